@@ -285,12 +285,20 @@ def _plain_write_one(x, codes, scale, bounds, start, n_blocks, kind):
     bi, ji = touched.nonzero(as_tuple=True)
     scale[bi, :, blk[bi, ji]] = s[bi, :, ji]
     if bounds is not None:
-        live = keep_new | keep_old
+        # a block that grew is summarised anew, else the older tokens'
+        # bounds are kept and widened
+        grew = (s > s_old)[..., None, None]
+        live = keep_new | (keep_old & grew)
         u = UNIT[kind]
         lo = torch.where(live, c, math.inf).amin(-2)
         hi = torch.where(live, c, -math.inf).amax(-2)
         bb = torch.stack([torch.floor(lo * u), torch.ceil(hi * u)],
                          -2).clamp(-127, 127)
+        was = bounds.transpose(1, 2)[rows, blk.clamp(0, nblk - 1)] \
+            .transpose(1, 2).float()
+        both = torch.stack([torch.minimum(bb[..., 0, :], was[..., 0, :]),
+                            torch.maximum(bb[..., 1, :], was[..., 1, :])], -2)
+        bb = torch.where(has_old[..., None, None] & ~grew, both, bb)
         bounds[bi, :, blk[bi, ji]] = bb[bi, :, ji].to(torch.int8)
 
 
