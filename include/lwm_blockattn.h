@@ -429,6 +429,109 @@ LWM_API int lwm_blockattn_decode(const void* q, const void* k_rot,
                                  void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/* ---------------------------------------------------------------------
+ * 8-bit KV cache: the cache of lwm_blockattn_decode held in 8 bits, with
+ * grouped query heads and, for long caches, attention over selected blocks.
+ *
+ * A cache of H heads and L slots per batch row (D == 128; a block is 128
+ * consecutive slots, nblk = ceil(L / 128); all memory the caller's):
+ *   k_cache, v_cache [B][H][L][D]      codes: e4m3 or int8 (cache_type)
+ *   k_scale, v_scale [B][H][nblk] f32  a code c stands for c * scale
+ *   k_bounds [B][H][nblk][2][D] int8   per channel the smallest ([0]) and
+ *     largest ([1]) key code of the block, rounded outwards, in units of
+ *     k_scale * Q / 127 (Q, the largest code: 448 for e4m3, 127 for int8)
+ * Tensors are 16-byte aligned; scales, positions, starts, lengths, block
+ * lists, scores and lse need 4 bytes only.
+ * Keys are stored rotated, in the rope_layout they came in. Scales of
+ * blocks that were never written should be 0 (a zeroed cache is a valid
+ * empty one). Query heads: Hq a multiple of H, at most 16 per cache head;
+ * query head i reads cache head i / (Hq / H). */
+typedef enum { LWM_KV8_E4M3 = 0, LWM_KV8_INT8 = 1 } lwm_kv8_type;
+
+/* Rotates and quantises new tokens into the cache.
+ *   k, v [B][T][H][D] bf16 (k un-rotated), positions [B][T] int32 in
+ *   [0, max_pos) with rope_table of max_pos positions;
+ *   start [B]: row b's token t goes to slot start[b] + t; slots outside
+ *   [0, L) are skipped; n_new [B] or NULL: only the first n_new[b] tokens
+ *   of a padded row are new (NULL: all T).
+ * Slots of a block below start are its older tokens; slots from start on
+ * count as empty before the call, whatever they hold, and those behind the
+ * last new token stay as they are. Per block and head touched, with x the
+ * rotated keys or the values in fp32 (products and sums rounded one by
+ * one): scale = max(the old scale if the block has older tokens,
+ * max|x| * (1/Q)), 0 if below 2^-126; code = round(x * (1/scale)), to
+ * nearest even; if the scale grew, older codes become
+ * round(code * (old/scale)) and the bounds are taken anew, else the bounds
+ * are widened by the new codes. A NaN or an infinity among the new values
+ * makes the block's scale NaN, and with it all that is read from the block.
+ * Two rows must not share memory. Async on stream. */
+LWM_API int lwm_kv8_write(const void* k, const void* v,
+                          const int32_t* positions, const int32_t* start,
+                          const int32_t* n_new, const float* rope_table,
+                          int max_pos, int B, int T, int L, int H, int D,
+                          int dtype, int cache_type, int rope_layout,
+                          void* k_cache, void* v_cache, float* k_scale,
+                          float* v_scale, int8_t* k_bounds, void* stream);
+
+/* Reads slots back: k_rot, v [B][T][H][D] bf16, the layout
+ * lwm_blockattn_fwd_block takes keys and values in. Token t of row b is
+ * slot start[b] + t; a slot outside [0, min(kv_len[b], L)) reads as zeros
+ * (kv_len NULL: L). Async on stream. */
+LWM_API int lwm_kv8_read(const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale,
+                         const int32_t* start, const int32_t* kv_len, int B,
+                         int T, int L, int H, int D, int dtype,
+                         int cache_type, void* k_rot, void* v, void* stream);
+
+/* Selects blocks for one query token per row: for each (b, cache head) the
+ * n_select blocks, among those that hold a slot of [kv_start[b],
+ * kv_len[b]), that score best, in ascending order:
+ *   blocks [B][H][n_select] int32, -1 behind the last of a short list;
+ *   scores [B][H][n_select] f32, -inf there.
+ * q, q_pos, rope_table as in lwm_kv8_decode. With q~ = R(q_pos) q in fp64
+ * and a = max|q~|: qi = round(q~ * (127 / a)) and score =
+ * sum_d max(qi_d lo_d, qi_d hi_d) * k_scale * (a * (1/127)), rounded once
+ * to fp32; of the query heads that share a cache head the largest. The
+ * first n_sink and the last n_recent visible blocks are always listed
+ * (n_sink + n_recent <= n_select), then blocks whose score is NaN; ties go
+ * to the lowest index. L <= 2^25. Async on stream. */
+LWM_API int lwm_kv8_select(const void* q, const int8_t* k_bounds,
+                           const float* k_scale, const int32_t* kv_start,
+                           const int32_t* kv_len, const int32_t* q_pos,
+                           const float* rope_table, int max_pos, int B, int L,
+                           int Hq, int H, int D, int dtype, int rope_layout,
+                           int n_select, int n_sink, int n_recent,
+                           int32_t* blocks, float* scores, void* stream);
+
+/* Bytes of workspace lwm_kv8_decode needs; n_blocks < 0 for a call without
+ * a block list. 0 for invalid sizes. */
+LWM_API size_t lwm_kv8_decode_workspace_size(int B, int L, int Hq, int H,
+                                             int D, int n_blocks);
+
+/* One query token per (b, query head) against the cache, as
+ * lwm_blockattn_decode:
+ *   q [B][Hq][D] bf16, un-rotated; kv_start, kv_len, q_pos [B] int32 (the
+ *   query sees slots [kv_start[b], kv_len[b]), clamped to [0, L]);
+ *   n_blocks < 0: every visible slot (blocks is not looked at); else
+ *   blocks [B][H][n_blocks] int32 lists the blocks whose visible slots are
+ *   read. A list is strictly ascending: an entry that is not above its left
+ *   neighbour, or that holds no visible slot (-1 too), is skipped.
+ *   out [B][Hq][D] bf16; lse [B][Hq] fp32 natural log over the slots read
+ *   (-inf, with out = 0, where there is none).
+ * Slots outside the range are never used, whatever they hold. Scores, the
+ * softmax and the sums are fp32. Async on stream; bounded waits report to
+ * lwm_blockattn_last_status. */
+LWM_API int lwm_kv8_decode(const void* q, const void* k_cache,
+                           const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int32_t* kv_start,
+                           const int32_t* kv_len, const int32_t* q_pos,
+                           const int32_t* blocks, int n_blocks,
+                           const float* rope_table, int max_pos, int B, int L,
+                           int Hq, int H, int D, int dtype, int cache_type,
+                           int rope_layout, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 /* Self-test of the failure path: launches one small CTA that waits on an
  * mbarrier nobody arrives on, with the same bounded wait the attention
  * kernels use and a limit of limit_ns nanoseconds (clamped to [1 ms, 2 s]).

@@ -39,6 +39,12 @@ __global__ void selftest_wait_kernel(int* status, uint64_t limit_ns) {
     mbar_wait(bar, 0, &abort_word, status, limit_ns);
 }
 
+int* status_word() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
+  return static_cast<int*>(p);
+}
+
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -163,12 +169,6 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? LWM_OK : LWM_ERR_CUDA
     cudaError_t e_ = (expr);                           \
     if (e_ != cudaSuccess) return LWM_ERR_CUDA;        \
   } while (0)
-
-int* status_word() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
-  return static_cast<int*>(p);
-}
 
 // Shared tail of lwm_blockattn_bwd and lwm_blockattn_bwd_block: key-side
 // metadata of queries [q_off, q_off+Nq) against keys [k_off, k_off+Nk), the

@@ -18,4 +18,8 @@ int check_fwd_args(const void* q, const void* k, const void* v,
                    int N, int H, int D, int dtype, int qk_precision,
                    int rope_layout, const void* out, const float* lse);
 
+// Device address of the status word that bounded waits report to (on the
+// current device), or null.
+int* status_word();
+
 }  // namespace lwm

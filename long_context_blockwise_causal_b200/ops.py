@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -23,6 +24,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, \
 DTYPE_BF16, DTYPE_FP32 = 0, 1
 QK_BF16, QK_BF16X3 = 0, 1
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+KV8_E4M3, KV8_INT8 = 0, 1
 TILE_EMPTY, TILE_PARTIAL, TILE_FULL = 0, 1, 2
 BLOCK = 128
 HEAD_DIM = 128
@@ -76,6 +78,12 @@ _SIGS = {
                                      _vp, _vp, _sz, _vp]),
     "lwm_blockattn_grad_finish": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                        _i, _vp, _vp]),
+    "lwm_kv8_write": (_i, [_vp] * 6 + [_i] * 9 + [_vp] * 6),
+    "lwm_kv8_read": (_i, [_vp] * 6 + [_i] * 7 + [_vp] * 3),
+    "lwm_kv8_select": (_i, [_vp] * 7 + [_i] * 11 + [_vp] * 3),
+    "lwm_kv8_decode_workspace_size": (_sz, [_i] * 6),
+    "lwm_kv8_decode": (_i, [_vp] * 9 + [_i, _vp] + [_i] * 9
+                       + [_vp, _vp, _vp, _sz, _vp]),
     "lwm_blockffn_workspace_size": (_sz, [_i, _i]),
     "lwm_blockffn_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
                               _vp, _sz, _vp]),
@@ -610,6 +618,197 @@ def decode(q, k_rot, v, kv_start, kv_len, q_pos, table, out=None, lse=None,
         _layout_code(rope_layout), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
         _stream(stream))
     _check(st, "lwm_blockattn_decode")
+    return out, lse
+
+
+class Kv8Cache(NamedTuple):
+    """An 8-bit KV cache: the caller's tensors, as the header lays them out.
+    k, v [B,H,L,D] torch.float8_e4m3fn or torch.int8; k_scale, v_scale
+    [B,H,ceil(L/128)] fp32; k_bounds [B,H,ceil(L/128),2,D] int8."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_bounds: torch.Tensor
+
+
+_KV8_TYPES = {torch.float8_e4m3fn: KV8_E4M3, torch.int8: KV8_INT8}
+
+
+def kv8_cache(B, L, H, dtype=torch.float8_e4m3fn, D=HEAD_DIM,
+              device="cuda") -> Kv8Cache:
+    """An empty (zeroed) cache of L slots and H heads per row."""
+    if dtype not in _KV8_TYPES:
+        raise TypeError(f"unsupported cache dtype {dtype}")
+    n = -(-L // BLOCK)
+    z = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
+    return Kv8Cache(z((B, H, L, D), dtype), z((B, H, L, D), dtype),
+                    z((B, H, n), torch.float32), z((B, H, n), torch.float32),
+                    z((B, H, n, 2, D), torch.int8))
+
+
+def _check_kv8(where, cache, *others):
+    """Shapes, types and placement of a cache; returns (B, H, L, D, type)."""
+    k, v, ks, vs, kb = cache
+    _expect_dims(where, "cache.k", k, 4)
+    code = _KV8_TYPES.get(k.dtype)
+    if code is None:
+        raise LwmError(ERR_INVALID_ARG, f"{where}: cache.k is {k.dtype}")
+    B, H, L, D = k.shape
+    n = -(-L // BLOCK)
+    _expect(where, "cache.v", v, k.shape, k.dtype)
+    _expect(where, "cache.k_scale", ks, (B, H, n), torch.float32)
+    _expect(where, "cache.v_scale", vs, (B, H, n), torch.float32)
+    _expect(where, "cache.k_bounds", kb, (B, H, n, 2, D), torch.int8)
+    _same_device(where, k, v, ks, vs, kb, *others)
+    return B, H, L, D, code
+
+
+def _check_kv8_query(where, q, B, H, D, kv_start, kv_len, q_pos, table):
+    """q [B,Hq,D] with Hq a multiple of H; returns Hq."""
+    _expect_dims(where, "q", q, 3)
+    _expect_dims(where, "table", table, 3)
+    Hq = q.shape[1]
+    _expect(where, "q", q, (B, Hq, D), torch.bfloat16)
+    if H and Hq % H:
+        raise LwmError(ERR_INVALID_ARG,
+                       f"{where}: {Hq} query heads over {H} cache heads")
+    for name, t in (("kv_start", kv_start), ("kv_len", kv_len),
+                    ("q_pos", q_pos)):
+        _expect(where, name, t, (B,), torch.int32)
+    _expect(where, "table", table, (table.shape[0], D // 2, 2),
+            torch.float32)
+    return Hq
+
+
+def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
+              rope_layout="interleaved"):
+    """Rotate and quantise k, v [B,T,H,D] bf16 into the cache at slots
+    start[b] + t (in place; see the header for the block scales). ``n_new``
+    [B]: new tokens of a padded row. Returns the cache."""
+    w = "kv8_write"
+    B, H, L, D, code = _check_kv8(w, cache, k, v, positions, start, table,
+                                  n_new)
+    _expect_dims(w, "k", k, 4)
+    _expect_dims(w, "table", table, 3)
+    T = k.shape[1]
+    _expect(w, "k", k, (B, T, H, D), torch.bfloat16)
+    _expect(w, "v", v, (B, T, H, D), torch.bfloat16)
+    _expect(w, "positions", positions, (B, T), torch.int32)
+    _expect(w, "start", start, (B,), torch.int32)
+    _expect(w, "n_new", n_new, (B,), torch.int32)
+    _expect(w, "table", table, (table.shape[0], D // 2, 2), torch.float32)
+    _need_cuda(*cache, k, v, positions, start, table, n_new)
+    with torch.cuda.device(k.device):
+        st = lib().lwm_kv8_write(
+            _ptr(k), _ptr(v), _ptr(positions), _ptr(start), _ptr(n_new),
+            _ptr(table), table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
+            _layout_code(rope_layout), _ptr(cache.k), _ptr(cache.v),
+            _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(cache.k_bounds),
+            _stream(stream))
+    _check(st, "lwm_kv8_write")
+    return cache
+
+
+def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
+    """Slots start[b] .. start[b] + T - 1 of the cache as (k_rot, v) bf16
+    [B,T,H,D], zeros outside [0, min(kv_len[b], L)); the layout fwd_block
+    takes rotated keys and values in."""
+    w = "kv8_read"
+    B, H, L, D, code = _check_kv8(w, cache, start, kv_len, k_rot, v)
+    _expect(w, "start", start, (B,), torch.int32)
+    _expect(w, "kv_len", kv_len, (B,), torch.int32)
+    T = int(T)
+    if T < 0:
+        raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
+    _expect(w, "k_rot", k_rot, (B, T, H, D), torch.bfloat16)
+    _expect(w, "v", v, (B, T, H, D), torch.bfloat16)
+    _need_cuda(*cache, start, kv_len, k_rot, v)
+    new = lambda: torch.empty((B, T, H, D), dtype=torch.bfloat16,
+                              device=cache.k.device)
+    k_rot = new() if k_rot is None else k_rot
+    v = new() if v is None else v
+    with torch.cuda.device(cache.k.device):
+        st = lib().lwm_kv8_read(
+            _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+            _ptr(cache.v_scale), _ptr(start), _ptr(kv_len), B, T, L, H, D,
+            DTYPE_BF16, code, _ptr(k_rot), _ptr(v), _stream(stream))
+    _check(st, "lwm_kv8_read")
+    return k_rot, v
+
+
+def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
+               n_recent=1, blocks=None, scores=None, stream=None,
+               rope_layout="interleaved"):
+    """The ``n_select`` blocks of 128 slots per (row, cache head) whose key
+    bounds admit the largest scores for q [B,Hq,D]: (blocks int32, scores
+    fp32) [B,H,n_select], ascending, (-1, -inf) behind a short list. The
+    first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
+    w = "kv8_select"
+    B, H, L, D, _ = _check_kv8(w, cache, q, kv_start, kv_len, q_pos, table,
+                               blocks, scores)
+    Hq = _check_kv8_query(w, q, B, H, D, kv_start, kv_len, q_pos, table)
+    K = int(n_select)
+    if K < 1:
+        raise LwmError(ERR_INVALID_ARG, f"{w}: n_select is {K}")
+    _expect(w, "blocks", blocks, (B, H, K), torch.int32)
+    _expect(w, "scores", scores, (B, H, K), torch.float32)
+    _need_cuda(*cache, q, kv_start, kv_len, q_pos, table, blocks, scores)
+    if blocks is None:
+        blocks = torch.empty((B, H, K), dtype=torch.int32, device=q.device)
+    if scores is None:
+        scores = torch.empty((B, H, K), dtype=torch.float32, device=q.device)
+    with torch.cuda.device(q.device):
+        st = lib().lwm_kv8_select(
+            _ptr(q), _ptr(cache.k_bounds), _ptr(cache.k_scale),
+            _ptr(kv_start), _ptr(kv_len), _ptr(q_pos), _ptr(table),
+            table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
+            _layout_code(rope_layout), K, int(n_sink), int(n_recent),
+            _ptr(blocks), _ptr(scores), _stream(stream))
+    _check(st, "lwm_kv8_select")
+    return blocks, scores
+
+
+def kv8_decode_workspace_size(B, L, Hq, H, n_blocks=None, D=HEAD_DIM) -> int:
+    return int(lib().lwm_kv8_decode_workspace_size(
+        B, L, Hq, H, D, -1 if n_blocks is None else n_blocks))
+
+
+def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
+               out=None, lse=None, workspace=None, stream=None,
+               rope_layout="interleaved"):
+    """One query token per (row, head), q [B,Hq,D], against slots
+    [kv_start[b], kv_len[b]) of an 8-bit cache, or only those of ``blocks``
+    [B,H,n] (a list of kv8_select, strictly ascending). Query head i reads
+    cache head i // (Hq // H). Returns (out [B,Hq,D], lse [B,Hq])."""
+    w = "kv8_decode"
+    B, H, L, D, code = _check_kv8(w, cache, q, kv_start, kv_len, q_pos,
+                                  table, blocks, out, lse, workspace)
+    Hq = _check_kv8_query(w, q, B, H, D, kv_start, kv_len, q_pos, table)
+    K = -1
+    if blocks is not None:
+        _expect_dims(w, "blocks", blocks, 3)
+        K = blocks.shape[2]
+        _expect(w, "blocks", blocks, (B, H, K), torch.int32)
+    _expect(w, "out", out, q.shape, q.dtype)
+    _expect(w, "lse", lse, (B, Hq), torch.float32)
+    _need_cuda(*cache, q, kv_start, kv_len, q_pos, table, blocks, out, lse,
+               workspace)
+    out = torch.empty_like(q) if out is None else out
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    ws = _workspace(int(lib().lwm_kv8_decode_workspace_size(B, L, Hq, H, D,
+                                                            K)),
+                    q.device, workspace)
+    with torch.cuda.device(q.device):
+        st = lib().lwm_kv8_decode(
+            _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+            _ptr(cache.v_scale), _ptr(kv_start), _ptr(kv_len), _ptr(q_pos),
+            _ptr(blocks), K, _ptr(table), table.shape[0], B, L, Hq, H, D,
+            DTYPE_BF16, code, _layout_code(rope_layout), _ptr(out),
+            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+            _stream(stream))
+    _check(st, "lwm_kv8_decode")
     return out, lse
 
 

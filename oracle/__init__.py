@@ -38,6 +38,7 @@ Modules:
                 a P-device ring run in order (RingAttention).
   classify   -- tile classification (brute force and a counting form).
   ffn        -- the blockwise (chunked) SwiGLU feed-forward network.
+  kv8        -- the 8-bit KV cache: codes, scales, selection and attention.
 """
 
 from .rope import (  # noqa: F401
@@ -56,6 +57,10 @@ from .ring import (  # noqa: F401
 from .ffn import (  # noqa: F401
     silu, swiglu_intermediate, swiglu_mlp, blockwise_mlp, silu_grad,
     swiglu_mlp_bwd,
+)
+from .kv8 import (  # noqa: F401
+    KV8_BLOCK, KV8_QMAX, kv8_half_step, kv8_encode, kv8_rotate,
+    kv8_block_scale, kv8_attend, kv8_block_scores, kv8_pick,
 )
 from .classify import (  # noqa: F401
     classify_bruteforce, classify_count, classify_cross, visible_key_ranges,
