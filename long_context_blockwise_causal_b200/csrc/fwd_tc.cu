@@ -911,6 +911,22 @@ bool make_2d_map_strided(CUtensorMap* m, const void* base, int64_t rows,
   return r == CUDA_SUCCESS;
 }
 
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t heads, int L) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cuuint64_t(kHeadDim), cuuint64_t(L),
+                        cuuint64_t(heads)};
+  cuuint64_t strides[2] = {cuuint64_t(kHeadDim), cuuint64_t(kHeadDim) * L};
+  cuuint32_t box[3] = {cuuint32_t(kHeadDim), cuuint32_t(kBlock), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // fp32 [B][N][H][128] tensor as a 4-D map {D, H, N, B}; box 32 x 1 x 32 x 1
 // (one 128-byte column chunk of 32 rows) with the 128-byte swizzle.
 bool make_bnhd_f32_map(CUtensorMap* m, const void* base, int B, int N,

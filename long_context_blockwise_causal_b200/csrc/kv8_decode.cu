@@ -85,163 +85,657 @@ __host__ __device__ constexpr int part_stride(int G) {
   return G * (kHeadDim + 2);
 }
 
-constexpr int kSimpleThreads = 128;
+// ---------------------------------------------------------------- kernel
+//
+// Both products run on the tensor cores straight on the codes, so no code
+// is ever converted on the CUDA cores:
+//   S[128 slots][n] = K tile (A, K-major)      . Q  (B: n rows of 128 codes)
+//   O[128 dims][n]  = V tile (A, read MN-major) . P  (B: n rows of 128 codes)
+// Q and P become codes of the cache's type: a number is the sum of a few
+// codes (terms), each carrying what the ones before it left, and each term
+// of each head is one column n; products of codes are exact and the columns
+// are added up in fp32. e4m3: terms 1/16 apart, 5 for q (2^-20 of a channel),
+// 3 for p (2^-12 of a weight). int8: terms 1/128 apart, 3 for q and 3 for p
+// (2^-21 of the largest). Weights are taken against the tile's own maximum,
+// so what a term cannot hold is small against the tile's own sum, however
+// far the running maximum lies above it.
+//
+// Warps 0-3: thread t is slot t of S (scores, maximum, weights) and channel
+// t of O (accumulator). Warp 4 issues the products, warp 5 walks the tiles
+// and loads them by TMA. The products of one tile run while the softmax
+// works on the next: S, P and O are double buffered.
+constexpr int kDecThreads = 192;
+constexpr int kDecRing = 8;              // tile descriptions
+constexpr uint64_t kDecWaitNs = 4000000000ull;
+constexpr int kTile = kKv8Block * kHeadDim;   // bytes of K or V of one tile
+
+enum : int {
+  kFirst = 1,     // first tile of its (row, head) in this CTA
+  kLast = 2,
+  kWhole = 4,     // the CTA holds every tile of the (row, head)
+  kSlot1 = 8,     // partial result goes to the CTA's second record
+  kEnd = 16,      // no tile: the CTA's work is done
+};
+struct __align__(16) Tile {
+  int b, h, blk, flags;
+  int lo, hi;     // visible slots of the block (lo >= hi: nothing to read)
+  float ks, vs;
+};
+
+template <bool kInt8, int GP>
+struct Dec {
+  static constexpr int kQTerms = kInt8 ? 3 : 5;
+  static constexpr int kPTerms = 3;
+  static constexpr int kNq = (kQTerms * GP + 15) / 16 * 16;
+  static constexpr int kNp = (kPTerms * GP + 15) / 16 * 16;
+  static constexpr int kCols = 2 * kNq + 2 * kNp;
+  static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+  static_assert(kCols <= 256, "two CTAs share the SM's 512 columns");
+  // factor from one term to the next, and of the first term
+  static constexpr float kStep = kInt8 ? 254.f : 16.f;
+  static constexpr float kPScale = kInt8 ? 127.f : 256.f;
+  static constexpr int kQExp = kInt8 ? 6 : 8;  // |q~| 2^(kQExp - e) < 2^kQExp
+  // shared memory, from a 1024-byte boundary
+  static constexpr int kQBytes = kNq * kHeadDim;
+  static constexpr int kPBytes = kNp * kKv8Block;
+  static constexpr int kSmall = 2 * kQBytes + 2 * kPBytes + 2048 +
+                                (2 * 4 + 2 + 4) * GP * 4;
+  // two CTAs per SM: as many stages as half of 227 KB holds
+  static constexpr int kStages = 3 * 2 * kTile + kSmall + 2048 <= 116000 ? 3
+                                                                         : 2;
+  static constexpr int kQ = kStages * 2 * kTile;
+  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kRingAt = kP + 2 * kPBytes;
+  static constexpr int kMaxAt = kRingAt + kDecRing * int(sizeof(Tile));
+  static constexpr int kQsAt = kMaxAt + 2 * 4 * GP * 4;
+  static constexpr int kSumAt = kQsAt + 2 * GP * 4;
+  static constexpr int kBars = (kSumAt + 4 * GP * 4 + 15) / 16 * 16;
+  static constexpr int bFull = 0, bEmpty = kStages, bTok = 2 * kStages,
+                       bS = bTok + kDecRing, bP = bS + 2, bO = bP + 2,
+                       bQ = bO + 2, bDone = bQ + 2, kNumBars = bDone + 1;
+  static constexpr int kTail = kBars + kNumBars * 8;  // tmem base, abort word
+  static constexpr int kSmem = kTail + 16 + 1024;
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+};
+
+// Byte (row, col) of a K-major operand of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ int sw128(int row, int col) {
+  return (row >> 3) * 1024 + (row & 7) * 128 +
+         ((((col >> 4) ^ (row & 7)) << 4) | (col & 15));
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                 : "=r"(r[0]) : "r"(at));
+  } else if constexpr (N == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, "
+        "[%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+          "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(at));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,"
+        "%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+          "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15])
+        : "r"(at));
+  }
+}
+
+// One 32-code step of a product: D[tmem] (+)= A . B^T.
+template <bool kInt8>
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b,
+                                     uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kInt8) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Instruction descriptor, M = 128: e4m3 x e4m3 -> f32, or s8 x s8 -> s32;
+// a_mn: A is MN-major. Fields as in idesc_bf16.
+template <bool kInt8>
+__device__ constexpr uint32_t idesc8(int N, int a_mn) {
+  return (kInt8 ? (2u << 4) | (1u << 7) | (1u << 10) : (1u << 4)) |
+         (uint32_t(a_mn) << 15) | (uint32_t(N >> 3) << 17) | (8u << 24);
+}
 
 template <bool kInt8>
-__global__ void __launch_bounds__(kSimpleThreads)
-kv8_decode_kernel(const Kv8DecodeArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float qs[kKv8MaxGroup][kHeadDim];
-  __shared__ float ps[kKv8MaxGroup][kKv8Block];
-  __shared__ float red[4];
-  __shared__ int64_t where[4];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const Rows rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K,
-                  a.listed};
-  if (warp == 0) {
-    const int64_t total = tiles_before(rows, a.B) * a.H;
-    const int64_t u0 = share(total, gridDim.x, blockIdx.x);
-    const int64_t u1 = share(total, gridDim.x, blockIdx.x + 1);
-    int64_t before = 0;
-    const int b = u0 < u1 ? find_row(rows, u0, &before) : 0;
-    if (lane == 0) {
-      where[0] = u0;
-      where[1] = u1;
-      where[2] = b;
-      where[3] = before;
+__device__ __forceinline__ float term_value(uint32_t w) {
+  return kInt8 ? float(int(w)) : __uint_as_float(w);
+}
+
+// Barrier of the softmax warps; true if all of their threads said so.
+__device__ __forceinline__ bool softmax_all(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(uint32_t(mine))
+      : "memory");
+  return all != 0;
+}
+
+// The next term of (a, b): its two codes, and what they leave, scaled up.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t next_term(float& a, float& b) {
+  constexpr float kStep = kInt8 ? 254.f : 16.f;
+  if constexpr (kInt8) {
+    const float ra = rintf(a), rb = rintf(b);
+    const uint32_t w = uint32_t(int(ra) & 255) | (uint32_t(int(rb) & 255) << 8);
+    a = (a - ra) * kStep;
+    b = (b - rb) * kStep;
+    return w;
+  } else {
+    const uint32_t w = enc2_e4m3(a, b);
+    const float2 f = dec2_e4m3(w);
+    a = (a - f.x) * kStep;
+    b = (b - f.y) * kStep;
+    return w;
+  }
+}
+
+// Walks the CTA's tiles: every readable one, and one empty tile for a
+// (row, head) whose list holds none.
+struct Walker {
+  Rows rows;
+  const int32_t* blocks;
+  int64_t u, u0, u1, row_at;
+  int b;
+  RowTiles rt;
+  // current (row, head): tiles [j, je) are left
+  int h, j, je, seg_flags;
+  bool emitted;
+
+  __device__ __forceinline__ void open() {   // at tile u < u1
+    while (u >= row_at + int64_t(rt.n) * rows.H) {
+      row_at += int64_t(rt.n) * rows.H;
+      rt = row_tiles(rows, ++b);
+    }
+    h = int((u - row_at) / rt.n);
+    const int64_t p0 = row_at + int64_t(h) * rt.n, p1 = p0 + rt.n;
+    j = int(u - p0);
+    je = int(min(u1, p1) - p0);
+    seg_flags = (p0 >= u0 && p1 <= u1 ? kWhole : 0) | (p0 < u0 ? 0 : kSlot1);
+    emitted = false;
+    u += je - j;
+  }
+  // False at the end of the CTA's share.
+  __device__ __forceinline__ bool next(Tile& t) {
+    for (;;) {
+      if (j >= je) {
+        if (!emitted && je >= 0) {            // nothing readable: one empty
+          emitted = true;
+          t.b = b; t.h = h; t.blk = 0; t.lo = t.hi = 0;
+          t.flags = seg_flags | kFirst;
+          return true;
+        }
+        if (u >= u1) return false;
+        open();
+        continue;
+      }
+      int blk = rt.t0 + j;
+      bool ok = true;
+      if (rows.listed) {
+        const int32_t* list =
+            blocks + (int64_t(b) * rows.H + h) * rows.K;
+        blk = __ldg(list + j);
+        ok = blk >= rt.t0 && int64_t(blk) * kKv8Block < rt.len &&
+             (j == 0 || blk > __ldg(list + j - 1));
+      }
+      ++j;
+      if (!ok) continue;
+      t.b = b; t.h = h; t.blk = blk;
+      t.lo = max(0, rt.start - blk * kKv8Block);
+      t.hi = min(kKv8Block, rt.len - blk * kKv8Block);
+      t.flags = seg_flags | (emitted ? 0 : kFirst);
+      emitted = true;
+      return true;
     }
   }
-  __syncthreads();
-  int64_t u = where[0];
-  const int64_t u0 = u, u1 = where[1];
-  int b = int(where[2]);
-  int64_t row_at = where[3];
-  const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
-  const float scale = kLog2e / sqrtf(float(kHeadDim));
-  auto reduce = [&](float x, bool is_max) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float y = __shfl_xor_sync(0xffffffffu, x, o);
-      x = is_max ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    return is_max ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]))
-                  : (red[0] + red[1]) + (red[2] + red[3]);
-  };
+};
 
-  while (u < u1) {
-    RowTiles rt = row_tiles(rows, b);
-    if (u >= row_at + int64_t(rt.n) * a.H) {
-      row_at += int64_t(rt.n) * a.H;
-      ++b;
-      continue;
+template <bool kInt8, int GP>
+__global__ void __launch_bounds__(kDecThreads, 2)
+kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ Kv8DecodeArgs a) {
+  using C = Dec<kInt8, GP>;
+  extern __shared__ uint8_t dsmem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  Tile* ring = reinterpret_cast<Tile*>(smem + C::kRingAt);
+  float* wmax = reinterpret_cast<float*>(smem + C::kMaxAt);   // [2][4][GP]
+  float* qscale = reinterpret_cast<float*>(smem + C::kQsAt);  // [2][GP]
+  float* wsum = reinterpret_cast<float*>(smem + C::kSumAt);   // [4][GP]
+  volatile int* abort_word =
+      reinterpret_cast<volatile int*>(smem + C::kTail + 4);
+  auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+
+  // set up while the kernel before this one may still run
+  if (t == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const bool by_warps = i >= C::bP && i < C::bP + 2;
+      const bool by_warps_q = i >= C::bQ && i < C::bQ + 2;
+      mbar_init(bar(i), by_warps || by_warps_q ? 4 : 1);
     }
-    const int h = int((u - row_at) / rt.n);
-    const int64_t p0 = row_at + int64_t(h) * rt.n, p1 = p0 + rt.n;
-    const int64_t ue = min(u1, p1);
-    const int64_t bh = int64_t(b) * a.H + h;
-    // rotated query
-    __syncthreads();
-    const int pos = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
-    for (int g = 0; g < a.G; ++g) {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                               (bh * a.G + g) * kHeadDim;
+    fence_mbar_init();
+    *abort_word = 0;
+  }
+  if (warp == 4) {
+    tmem_alloc(sbase + C::kTail, C::kTmem);
+    tmem_relinquish();
+  }
+  if (warp == 5 && lane == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + C::kTail);
+  pdl_wait();
+  pdl_trigger();
+  auto wait = [&](int i, int phase) {
+    return mbar_wait(bar(i), phase & 1, abort_word, a.status, kDecWaitNs);
+  };
+  const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
+
+  if (warp == 5) {
+    // ------------------------------------------------------ tiles and TMA
+    Walker w;
+    w.rows = Rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
+    w.blocks = a.blocks;
+    const int64_t total = tiles_before(w.rows, a.B) * a.H;
+    w.u0 = w.u = share(total, gridDim.x, blockIdx.x);
+    w.u1 = share(total, gridDim.x, blockIdx.x + 1);
+    w.b = w.u < w.u1 ? find_row(w.rows, w.u, &w.row_at) : 0;
+    w.j = 0;
+    w.je = -1;
+    w.emitted = true;
+    if (lane == 0) {
+      if (w.u < w.u1) w.rt = row_tiles(w.rows, w.b);
+      Tile cur, nxt;
+      bool more = w.next(cur);
+      int i = 0;
+      bool ok = true;
+      for (; more && ok; ++i) {
+        const int s = i % C::kStages;
+        const bool live = cur.lo < cur.hi;
+        const int64_t bh = int64_t(cur.b) * a.H + cur.h;
+        if (live) {
+          cur.ks = __ldg(a.k_scale + bh * nblk + cur.blk);
+          cur.vs = __ldg(a.v_scale + bh * nblk + cur.blk);
+        }
+        more = w.next(nxt);
+        if (!more || (nxt.flags & kFirst)) cur.flags |= kLast;
+        if (i >= C::kStages) ok = wait(C::bEmpty + s, i / C::kStages - 1);
+        if (!ok) break;
+        if (live) {
+          const uint32_t at = sbase + s * 2 * kTile;
+          mbar_arrive_expect_tx(bar(C::bFull + s), 2 * kTile);
+          tma_load_3d(at, &tm_k, bar(C::bFull + s), 0, cur.blk * kKv8Block,
+                      int(bh));
+          tma_load_3d(at + kTile, &tm_v, bar(C::bFull + s), 0,
+                      cur.blk * kKv8Block, int(bh));
+        } else {
+          mbar_arrive(bar(C::bFull + s));
+        }
+        ring[i % kDecRing] = cur;
+        mbar_arrive(bar(C::bTok + i % kDecRing));
+        cur = nxt;
+      }
+      if (ok) {
+        ring[i % kDecRing].flags = kEnd;
+        mbar_arrive(bar(C::bTok + i % kDecRing));
+      }
+      // no load is in flight when the CTA leaves, abandoned or not
+      for (int f = max(0, i - C::kStages); f < i; ++f)
+        mbar_wait(bar(C::bFull + f % C::kStages), (f / C::kStages) & 1,
+                  nullptr, a.status, kDecWaitNs);
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idq = idesc8<kInt8>(C::kNq, 0);
+      constexpr uint32_t idp = idesc8<kInt8>(C::kNp, 1);
+      int seg = -1;
+      // scores of tile i
+      auto qk = [&](int i) {
+        if (!wait(C::bTok + i % kDecRing, i / kDecRing)) return 2;
+        const int flags = ring[i % kDecRing].flags;
+        if (flags & kEnd) return 1;
+        const bool live = ring[i % kDecRing].lo < ring[i % kDecRing].hi;
+        const int s = i % C::kStages;
+        if (flags & kFirst) {
+          ++seg;
+          if (!wait(C::bQ + (seg & 1), seg >> 1)) return 2;
+        }
+        if (!wait(C::bFull + s, i / C::kStages)) return 2;
+        tc_fence_after();
+        if (live) {
+          const uint64_t kd = sdesc_sw128(sbase + s * 2 * kTile, 16, 1024);
+          const uint64_t qd =
+              sdesc_sw128(sbase + C::kQ + (seg & 1) * C::kQBytes, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 32; ++k)
+            mma8<kInt8>(tmem + (i & 1) * C::kNq, kd + 2 * k, qd + 2 * k, idq,
+                        k > 0);
+        }
+        mma_commit(bar(C::bS + (i & 1)));
+        return 0;
+      };
+      // weights times values of tile i
+      auto pv = [&](int i) {
+        if (!wait(C::bP + (i & 1), i >> 1)) return false;
+        tc_fence_after();
+        const int s = i % C::kStages;
+        if (ring[i % kDecRing].lo < ring[i % kDecRing].hi) {
+          const uint64_t vd =
+              sdesc_sw128(sbase + s * 2 * kTile + kTile, kTile, 1024);
+          const uint64_t pd =
+              sdesc_sw128(sbase + C::kP + (i & 1) * C::kPBytes, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kKv8Block / 32; ++k)
+            mma8<kInt8>(tmem + 2 * C::kNq + (i & 1) * C::kNp,
+                        vd + uint64_t(k * (32 * kHeadDim >> 4)), pd + 2 * k,
+                        idp, k > 0);
+        }
+        mma_commit(bar(C::bEmpty + s));
+        mma_commit(bar(C::bO + (i & 1)));
+        return true;
+      };
+      int state = qk(0);
+      for (int i = 0; state == 0; ++i) {
+        // the next tile's scores go first, unless they wait for a query
+        // that the softmax makes after this tile's weights
+        const bool last = ring[i % kDecRing].flags & kLast;
+        if (!last && (state = qk(i + 1)) == 2) break;
+        if (!pv(i)) break;
+        if (last) state = qk(i + 1);
+      }
+      // no product is running when the CTA leaves
+      mma_commit(bar(C::bDone));
+      mbar_wait(bar(C::bDone), 0, nullptr, a.status, kDecWaitNs);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const uint32_t my_tmem = tmem + (uint32_t(warp * 32) << 16);
+    int seg = -1;
+    // Query of a (row, head): rotated, split into terms, thread t channel t.
+    auto make_q = [&](int b, int h, int buf) {
+      const int pos = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
       const int k = a.half ? (t & 63) : (t >> 1);
       const bool low = a.half ? t < 64 : (t & 1) == 0;
       const int ia = a.half ? k : 2 * k, ib = a.half ? k + 64 : 2 * k + 1;
       const float2 cs = __ldg(reinterpret_cast<const float2*>(a.table) +
                               int64_t(pos) * (kHeadDim / 2) + k);
-      const float qa = __bfloat162float(q[ia]), qb = __bfloat162float(q[ib]);
-      qs[g][t] = (low ? qa * cs.x - qb * cs.y : qa * cs.y + qb * cs.x) * scale;
-    }
-    __syncthreads();
-    float m[kKv8MaxGroup], l[kKv8MaxGroup], acc[kKv8MaxGroup];
-    for (int g = 0; g < kKv8MaxGroup; ++g) {
-      m[g] = -INFINITY;
-      l[g] = 0.f;
-      acc[g] = 0.f;
-    }
-    for (; u < ue; ++u) {
-      const int j = int(u - p0);
-      int blk = rt.t0 + j;
-      if (a.listed) {
-        const int32_t* list = a.blocks + bh * a.K;
-        blk = __ldg(list + j);
-        if (blk < rt.t0 || int64_t(blk) * kKv8Block >= rt.len ||
-            (j > 0 && blk <= __ldg(list + j - 1)))
-          continue;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                               (int64_t(b) * a.H + h) * a.G * kHeadDim;
+      float x[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        x[g] = 0.f;
+        if (g < a.G) {
+          const float qa = __bfloat162float(q[g * kHeadDim + ia]);
+          const float qb = __bfloat162float(q[g * kHeadDim + ib]);
+          x[g] = low ? qa * cs.x - qb * cs.y : qa * cs.y + qb * cs.x;
+        }
       }
-      const int slot = blk * kKv8Block + t;
-      const bool seen = slot >= rt.start && slot < rt.len;
-      const float ks = __ldg(a.k_scale + bh * nblk + blk);
-      const float vs = __ldg(a.v_scale + bh * nblk + blk);
-      float s[kKv8MaxGroup];
-      for (int g = 0; g < kKv8MaxGroup; ++g) s[g] = 0.f;
-      if (seen) {
-        const uint4* kr = reinterpret_cast<const uint4*>(
-            static_cast<const uint8_t*>(a.k) +
-            (bh * a.L + slot) * kHeadDim);
-        for (int i = 0; i < 8; ++i) {
-          const uint4 w = __ldg(kr + i);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = dec2<kInt8>((ws[e >> 1] >> (16 * (e & 1))) &
-                                         0xffffu);
-            for (int g = 0; g < a.G; ++g) {
-              s[g] = fmaf(f.x, qs[g][16 * i + 2 * e], s[g]);
-              s[g] = fmaf(f.y, qs[g][16 * i + 2 * e + 1], s[g]);
+      float big[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        // a NaN or an infinity counts as the largest magnitude
+        const float m = fabsf(x[g]);
+        big[g] = warp_max(m <= 3.402823466e38f ? m : INFINITY);
+      }
+      if (lane == 0)
+#pragma unroll
+        for (int g = 0; g < GP; ++g) wsum[warp * GP + g] = big[g];
+      named_barrier_sync(1, 128);
+      float y[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float m = fmaxf(fmaxf(wsum[g], wsum[GP + g]),
+                              fmaxf(wsum[2 * GP + g], wsum[3 * GP + g]));
+        const bool fine = m <= 3.402823466e38f;
+        // m < 2^e
+        const int e = int(__float_as_uint(m) >> 23) - 126;
+        y[g] = fine ? ldexpf(x[g], C::kQExp - e) : 0.f;
+        if (t == 0)
+          qscale[buf * GP + g] =
+              fine ? ldexpf(kLog2e / sqrtf(float(kHeadDim)), e - C::kQExp)
+                   : __int_as_float(0x7fffffff);
+      }
+      uint8_t* dst = smem + C::kQ + buf * C::kQBytes;
+#pragma unroll
+      for (int n = 0; n < C::kQTerms; ++n) {
+#pragma unroll
+        for (int g = 0; g < GP; g += 2) {
+          float dummy = 0.f;
+          const uint32_t w =
+              next_term<kInt8>(y[g], g + 1 < GP ? y[(g + 1) % GP] : dummy);
+          dst[sw128(n * GP + g, t)] = uint8_t(w);
+          if (g + 1 < GP) dst[sw128(n * GP + g + 1, t)] = uint8_t(w >> 8);
+        }
+      }
+      fence_proxy_async_smem();
+      // all of wsum has been read and qscale written before anyone goes on
+      named_barrier_sync(1, 128);
+      if (lane == 0) mbar_arrive(bar(C::bQ + buf));
+    };
+
+    float m[GP], l[GP], acc[GP], alpha[GP], beta[GP];
+    bool pending = false;
+    // a wait that gave up is agreed on at the next barrier of these warps,
+    // so that none is left at a barrier alone
+    bool ok = wait(C::bTok, 0);
+    bool go = softmax_all(ok);
+    Tile cur = ring[0];
+    if (go && !(cur.flags & kEnd)) {
+      make_q(cur.b, cur.h, 0);
+      seg = 0;
+    }
+    // adds the product of tile i, whose weights were scaled by alpha, beta
+    auto add_o = [&](int i, bool live) {
+      ok = wait(C::bO + (i & 1), i >> 1) && ok;
+      if (!live) return;
+      tc_fence_after();
+      uint32_t r[C::kPTerms][GP];
+      const uint32_t at = my_tmem + 2 * C::kNq + (i & 1) * C::kNp;
+#pragma unroll
+      for (int n = 0; n < C::kPTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        float o = term_value<kInt8>(r[C::kPTerms - 1][g]);
+#pragma unroll
+        for (int n = C::kPTerms - 2; n >= 0; --n)
+          o = fmaf(o, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
+        acc[g] = fmaf(o, beta[g], acc[g] * alpha[g]);
+      }
+      tc_fence_before();
+    };
+
+    for (int i = 0; go && !(cur.flags & kEnd); ++i) {
+      const bool live = cur.lo < cur.hi;
+      ok = wait(C::bTok + (i + 1) % kDecRing, (i + 1) / kDecRing) && ok;
+      const Tile nxt = ring[(i + 1) % kDecRing];
+      if (cur.flags & kFirst) {
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          m[g] = -INFINITY;
+          l[g] = 0.f;
+          acc[g] = 0.f;
+        }
+      }
+      ok = wait(C::bS + (i & 1), i >> 1) && ok;
+      tc_fence_after();
+      if (!live) {
+        go = softmax_all(ok);
+        if (!go) break;
+      }
+      float al[GP], be[GP];
+      if (live) {
+        float s[GP];
+        {
+          const uint32_t at = my_tmem + (i & 1) * C::kNq;
+          uint32_t r[C::kQTerms][GP];
+#pragma unroll
+          for (int n = 0; n < C::kQTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
+          tmem_wait_ld();
+          tc_fence_before();
+          const bool seen = t >= cur.lo && t < cur.hi;
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            float x = term_value<kInt8>(r[C::kQTerms - 1][g]);
+#pragma unroll
+            for (int n = C::kQTerms - 2; n >= 0; --n)
+              x = fmaf(x, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
+            s[g] = seen ? x * (cur.ks * qscale[(seg & 1) * GP + g])
+                        : -INFINITY;
+          }
+        }
+        float* wm = wmax + (i & 1) * 4 * GP;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          const float x = warp_max(s[g]);
+          if (lane == 0) wm[warp * GP + g] = x;
+        }
+        go = softmax_all(ok);
+        if (!go) break;
+        float p[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          const float mt = fmaxf(fmaxf(wm[g], wm[GP + g]),
+                                 fmaxf(wm[2 * GP + g], wm[3 * GP + g]));
+          const float mn = fmaxf(m[g], mt);
+          const float mu = mn == -INFINITY ? 0.f : mn;
+          al[g] = exp2f(m[g] - mu);
+          be[g] = exp2f(mt - mu);
+          p[g] = exp2f(s[g] - (mt == -INFINITY ? 0.f : mt));
+          m[g] = mn;
+          l[g] = fmaf(p[g], be[g], l[g] * al[g]);
+          p[g] *= C::kPScale;
+          be[g] *= cur.vs * (1.f / C::kPScale);
+        }
+        uint8_t* dst = smem + C::kP + (i & 1) * C::kPBytes;
+#pragma unroll
+        for (int n = 0; n < C::kPTerms; ++n) {
+#pragma unroll
+          for (int g = 0; g < GP; g += 2) {
+            float dummy = 0.f;
+            const uint32_t w =
+                next_term<kInt8>(p[g], g + 1 < GP ? p[(g + 1) % GP] : dummy);
+            dst[sw128(n * GP + g, t)] = uint8_t(w);
+            if (g + 1 < GP) dst[sw128(n * GP + g + 1, t)] = uint8_t(w >> 8);
+          }
+        }
+        if (!kInt8 && (t < cur.lo || t >= cur.hi)) {
+          // an unseen slot's weight is 0, but its codes may be NaN (the
+          // tile is in place: its barrier has flipped, S came after it)
+          wait(C::bFull + i % C::kStages, i / C::kStages);
+          uint4* row = reinterpret_cast<uint4*>(
+              smem + (i % C::kStages) * 2 * kTile + kTile + t * kHeadDim);
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 16; ++k)
+            row[k] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::bP + (i & 1)));
+      // the next (row, head)'s query
+      if (!(nxt.flags & kEnd) && (nxt.flags & kFirst))
+        make_q(nxt.b, nxt.h, (seg + 1) & 1);
+      // the product of the tile before ran meanwhile
+      if (pending) add_o(i - 1, true);
+      pending = live;
+      if (live) {
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          alpha[g] = al[g];
+          beta[g] = be[g];
+        }
+      }
+      if (cur.flags & kLast) {
+        add_o(i, live);
+        pending = false;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          float x = l[g];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+          if (lane == 0) wsum[warp * GP + g] = x;
+        }
+        named_barrier_sync(1, 128);
+        const int64_t o0 = (int64_t(cur.b) * a.H + cur.h) * a.G;
+        float* rec = a.part + (int64_t(blockIdx.x) * 2 +
+                               ((cur.flags & kSlot1) ? 1 : 0)) *
+                                  part_stride(a.G);
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          if (g >= a.G) break;
+          const float lt = (wsum[g] + wsum[GP + g]) +
+                           (wsum[2 * GP + g] + wsum[3 * GP + g]);
+          if (cur.flags & kWhole) {
+            static_cast<__nv_bfloat16*>(a.out)[(o0 + g) * kHeadDim + t] =
+                __float2bfloat16_rn(lt == 0.f ? 0.f : acc[g] / lt);
+            if (t == 0)
+              a.lse[o0 + g] =
+                  lt == 0.f ? -INFINITY : (m[g] + log2f(lt)) * kLn2;
+          } else {
+            rec[2 * a.G + g * kHeadDim + t] = acc[g];
+            if (t == 0) {
+              rec[g] = m[g];
+              rec[a.G + g] = lt;
             }
           }
         }
+        named_barrier_sync(1, 128);   // wsum is free again
+        ++seg;
       }
-      for (int g = 0; g < a.G; ++g) {
-        const float x = seen ? s[g] * ks : -INFINITY;
-        const float mn = fmaxf(m[g], reduce(x, true));
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float alpha = exp2f(m[g] - mu);
-        const float p = seen ? exp2f(x - mu) : 0.f;
-        m[g] = mn;
-        l[g] = l[g] * alpha + p;
-        acc[g] *= alpha;
-        ps[g][t] = p;
-      }
-      __syncthreads();
-      // thread t: channel t
-      const int lo = max(0, rt.start - blk * kKv8Block);
-      const int hi = min(kKv8Block, rt.len - blk * kKv8Block);
-      float o[kKv8MaxGroup];
-      for (int g = 0; g < kKv8MaxGroup; ++g) o[g] = 0.f;
-      const uint8_t* vr = static_cast<const uint8_t*>(a.v) +
-                          (bh * a.L + int64_t(blk) * kKv8Block) * kHeadDim;
-      for (int i = lo; i < hi; ++i) {
-        const float f = dec2<kInt8>(vr[i * kHeadDim + t]).x;
-        for (int g = 0; g < a.G; ++g) o[g] = fmaf(f, ps[g][i], o[g]);
-      }
-      for (int g = 0; g < a.G; ++g) acc[g] = fmaf(o[g], vs, acc[g]);
-      __syncthreads();
+      cur = nxt;
     }
-    const bool whole = p0 >= u0 && p1 <= u1;
-    float* rec = a.part + (int64_t(blockIdx.x) * 2 + (p0 < u0 ? 0 : 1)) *
-                              part_stride(a.G);
-    for (int g = 0; g < a.G; ++g) {
-      const float lt = reduce(l[g], false);
-      if (whole) {
-        const int64_t o = bh * a.G + g;
-        static_cast<__nv_bfloat16*>(a.out)[o * kHeadDim + t] =
-            __float2bfloat16_rn(lt == 0.f ? 0.f : acc[g] / lt);
-        if (t == 0)
-          a.lse[o] = lt == 0.f ? -INFINITY : (m[g] + log2f(lt)) * kLn2;
-      } else {
-        rec[2 * a.G + g * kHeadDim + t] = acc[g];
-        if (t == 0) {
-          rec[g] = m[g];
-          rec[a.G + g] = lt;
-        }
-      }
-    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -308,20 +802,52 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
 }  // namespace
 
 int kv8_decode_grid(int B, int L, int H, int K) {
+  // two CTAs per SM, never more than there can be tiles
   const int64_t per = K >= 0 ? K : (L + kKv8Block - 1) / kKv8Block;
   const int64_t most = int64_t(B) * H * per;
-  return int(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 8)));
+  return int(std::max<int64_t>(1, std::min<int64_t>(most, 2 * sm_count())));
 }
 
 size_t kv8_part_floats(int B, int L, int H, int G, int K) {
   return size_t(kv8_decode_grid(B, L, H, K)) * 2 * part_stride(G);
 }
 
+namespace {
+
+template <bool kInt8, int GP>
+cudaError_t launch_tiles(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
+  using D = Dec<kInt8, GP>;
+  CUtensorMap mk, mv;
+  // an empty cache issues no load; the maps then only need valid shapes
+  const void* k = a.L > 0 ? a.k : a.part;
+  const void* v = a.L > 0 ? a.v : a.part;
+  const int L = std::max(a.L, 1);
+  if (!make_codes_map(&mk, k, int64_t(a.B) * a.H, L) ||
+      !make_codes_map(&mv, v, int64_t(a.B) * a.H, L))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(
+      kv8_decode_kernel<kInt8, GP>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kv8_decode_kernel<kInt8, GP>, dim3(C),
+                          dim3(kDecThreads), D::kSmem, st, mk, mv, a);
+}
+
+template <bool kInt8>
+cudaError_t launch_group(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
+  if (a.G == 1) return launch_tiles<kInt8, 1>(a, C, st);
+  if (a.G == 2) return launch_tiles<kInt8, 2>(a, C, st);
+  if (a.G <= 4) return launch_tiles<kInt8, 4>(a, C, st);
+  if (a.G <= 8) return launch_tiles<kInt8, 8>(a, C, st);
+  return launch_tiles<kInt8, 16>(a, C, st);
+}
+
+}  // namespace
+
 cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
   const int C = kv8_decode_grid(a.B, a.L, a.H, a.listed ? a.K : -1);
-  cudaError_t e = launch_dependent(
-      a.int8 ? kv8_decode_kernel<true> : kv8_decode_kernel<false>, dim3(C),
-      dim3(kSimpleThreads), 0, st, a);
+  cudaError_t e =
+      a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;
   note_launch();
   e = launch_dependent(kv8_combine_kernel, dim3(a.B * a.H), dim3(kHeadDim), 0,

@@ -93,6 +93,9 @@ bool make_2d_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
                  int box_rows);
 bool make_2d_map_strided(CUtensorMap* m, const void* base, int64_t rows,
                          int64_t cols, int64_t ld, int box_rows);
+// Codes of an 8-bit cache, bytes [heads][L][128], as a 3-D map; box 128
+// bytes x 128 rows x 1 with the 128-byte swizzle. Rows past L read as 0.
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t heads, int L);
 int sm_count();
 cudaError_t launch_bwd_tc(const BwdArgs& a, cudaStream_t st);
 

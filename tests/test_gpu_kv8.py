@@ -7,10 +7,18 @@ Tolerances, from the roundings that the calls make (bf16 is off by at most
   step, plus the fp32 error of x / s. The rotation rounds cos, sin, two
   products and a sum, at most 2^-22 of the pair's length, which is at most
   sqrt(2) Q in codes; 1 / s and the product with it add 2^-23 of the code.
-* scores: the query is rounded to 2^-20 of each channel and rotated with
-  2^-22, products are exact and sums fp32, so a score is off by at most
-  DS = 2^-18 sum |q_d k_d| / sqrt(D); weights are then off by 2 DS and by
-  the 2^-12 to which they enter the second product.
+* scores: the query is rounded to 2^-20 of each channel (int8: 2^-22 of the
+  largest) and rotated with 2^-22, products are exact and sums fp32, so a
+  score is off by at most DS = 2^-18 sum (|q_d| + max|q| / 16) |k_d| /
+  sqrt(D); weights are then off by 2 DS and by the 2^-12 to which they enter
+  the second product.
+* a weight below 2^-13 of the largest one of its block enters the second
+  product as a multiple of a fixed fraction of that one: int8 codes hold
+  p 127 in three parts 1/254 apart, a last step of 1 / (127 254^2) < 2^-22.9
+  and half of it at most 2^-23.9; e4m3 codes hold p 256 in three parts 1/16
+  apart with a smallest step of 2^-9, 2^-9 / 256 / 256 = 2^-25 and half of
+  it 2^-26. So each value may be off by 2^-23 |v_t| times the largest weight
+  of its block, whatever its own weight is.
 """
 
 import numpy as np
@@ -304,10 +312,17 @@ def check_decode(c, q, pos, table, start, length, layout, blocks=None,
                     assert (go[b, i] == 0).all() and gl[b, i] == -np.inf
                     continue
                 ds = 2 ** -18 * float(
-                    (np.abs(k[b, h][slots]) @ np.abs(qr[i])
+                    (np.abs(k[b, h][slots]) @ (np.abs(qr[i])
+                                               + np.abs(qr[i]).max() / 16)
                      * ks[b, h][slots // 128]).max()) / np.sqrt(D)
                 assert abs(gl[b, i] - l) <= ds + 2 ** -20 * (1 + abs(l))
-                tol = 2 ** -8 * np.abs(o) + (2 ** -11 + 4 * ds) * w
+                floor = sum(np.abs(v[b, h][slots[slots // 128 == j]]).sum(0)
+                            * vs[b, h][j] * np.exp(oracle.kv8_attend(
+                                qr[i], k[b, h], v[b, h], ks[b, h], vs[b, h],
+                                slots[slots // 128 == j])[1] - l)
+                            for j in np.unique(slots // 128))
+                tol = 2 ** -8 * np.abs(o) + (2 ** -11 + 4 * ds) * w + \
+                    2 ** -23 * floor
                 assert (np.abs(go[b, i] - o) <= tol).all(), \
                     (b, i, np.abs(go[b, i] - o).max())
     return out, lse
