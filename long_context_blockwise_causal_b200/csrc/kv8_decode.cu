@@ -18,6 +18,12 @@
 namespace lwm {
 namespace {
 
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 struct Rows {
   const int32_t* kv_start;
   const int32_t* kv_len;
@@ -75,14 +81,27 @@ __device__ __forceinline__ int find_row(const Rows& r, int64_t u,
   return r.B;
 }
 
-// CTA c of C takes tiles [share(c), share(c + 1)).
-__device__ __forceinline__ int64_t share(int64_t total, int C, int c) {
-  return total * c / C;
-}
+// CTA c of C takes tiles [first(c), first(c + 1)): the first `more` CTAs
+// take one tile more than the others.
+struct Shares {
+  int64_t each;
+  int more;
+  __device__ __forceinline__ Shares(int64_t total, int C)
+      : each(total / C), more(int(total - each * C)) {}
+  __device__ __forceinline__ int64_t first(int c) const {
+    return each * c + min(c, more);
+  }
+  // The CTA that holds tile u.
+  __device__ __forceinline__ int holder(int64_t u) const {
+    const int64_t cut = (each + 1) * more;
+    return u < cut ? int(u / (each + 1)) : more + int((u - cut) / each);
+  }
+};
 
-// Partial result records: m[G], l[G], acc[G][128].
+// Partial result records: m[G], l[G], padding to 16 bytes, acc[G][128].
+__host__ __device__ constexpr int part_acc(int G) { return (2 * G + 3) & ~3; }
 __host__ __device__ constexpr int part_stride(int G) {
-  return G * (kHeadDim + 2);
+  return part_acc(G) + G * kHeadDim;
 }
 
 // ---------------------------------------------------------------- kernel
@@ -162,12 +181,6 @@ struct Dec {
 __device__ __forceinline__ int sw128(int row, int col) {
   return (row >> 3) * 1024 + (row & 7) * 128 +
          ((((col >> 4) ^ (row & 7)) << 4) | (col & 15));
-}
-
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
 }
 
 template <int N>
@@ -379,8 +392,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     w.rows = Rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
     w.blocks = a.blocks;
     const int64_t total = tiles_before(w.rows, a.B) * a.H;
-    w.u0 = w.u = share(total, gridDim.x, blockIdx.x);
-    w.u1 = share(total, gridDim.x, blockIdx.x + 1);
+    const Shares sh(total, gridDim.x);
+    w.u0 = w.u = sh.first(blockIdx.x);
+    w.u1 = sh.first(blockIdx.x + 1);
     w.b = w.u < w.u1 ? find_row(w.rows, w.u, &w.row_at) : 0;
     w.j = 0;
     w.je = -1;
@@ -718,7 +732,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
               a.lse[o0 + g] =
                   lt == 0.f ? -INFINITY : (m[g] + log2f(lt)) * kLn2;
           } else {
-            rec[2 * a.G + g * kHeadDim + t] = acc[g];
+            rec[part_acc(a.G) + g * kHeadDim + t] = acc[g];
             if (t == 0) {
               rec[g] = m[g];
               rec[a.G + g] = lt;
@@ -739,64 +753,103 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 }
 
-// One CTA per (row, cache head): joins the parts of a (row, head) that more
-// than one CTA of the decode kernel worked on, and writes (0, -inf) for a
-// row that sees nothing.
-__global__ void __launch_bounds__(kHeadDim)
+// One CTA per (row, query head): joins the parts of a (row, cache head) that
+// more than one CTA of the decode kernel worked on, and writes (0, -inf) for
+// a row that sees nothing. A pass takes up to 64 parts: their maxima and
+// sums by one thread each, their accumulators by eight groups of 32 lanes
+// (four channels per lane), every group an eighth of the parts.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = kJoinThreads / 32;
+constexpr int kJoinParts = 64;
+
+__global__ void __launch_bounds__(kJoinThreads)
 kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
   pdl_wait();
   pdl_trigger();
   __shared__ int64_t where[2];
-  const int t = threadIdx.x;
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const Rows rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K,
-                  a.listed};
-  if (t < 32) {
-    const int64_t total = tiles_before(rows, a.B) * a.H;
-    const int64_t before = tiles_before(rows, b) * a.H;
-    if (t == 0) {
-      where[0] = total;
-      where[1] = before;
-    }
+  __shared__ float wt[kJoinParts];
+  __shared__ float4 part[kJoinGroups][32];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int bh = blockIdx.x / a.G, g = blockIdx.x - bh * a.G;
+  const int b = bh / a.H, h = bh - b * a.H;
+  const Rows rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
+  if (warp < 2) {
+    const int64_t n = tiles_before(rows, warp == 0 ? a.B : b) * a.H;
+    if (lane == 0) where[warp] = n;
   }
-  __syncthreads();
-  const int64_t total = where[0];
   const int n = row_tiles(rows, b).n;
-  const int64_t o0 = int64_t(blockIdx.x) * a.G;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                       int64_t(blockIdx.x) * kHeadDim;
   if (n == 0) {
-    for (int g = 0; g < a.G; ++g) {
-      static_cast<__nv_bfloat16*>(a.out)[(o0 + g) * kHeadDim + t] =
-          __float2bfloat16_rn(0.f);
-      if (t == 0) a.lse[o0 + g] = -INFINITY;
-    }
+    if (t < kHeadDim) out[t] = __float2bfloat16_rn(0.f);
+    if (t == 0) a.lse[blockIdx.x] = -INFINITY;
     return;
   }
-  const int64_t p0 = where[1] + int64_t(h) * n, p1 = p0 + n;
-  const int c0 = int(((p0 + 1) * C - 1) / total);
-  const int c1 = int((p1 * C - 1) / total);
+  __syncthreads();
+  const Shares sh(where[0], C);
+  const int64_t p0 = where[1] + int64_t(h) * n;
+  const int c0 = sh.holder(p0), c1 = sh.holder(p0 + n - 1);
   if (c0 == c1) return;       // one CTA held it all
-  for (int g = 0; g < a.G; ++g) {
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      if (share(total, C, c) == share(total, C, c + 1)) continue;
-      const float* rec =
-          a.part + (int64_t(c) * 2 + (c == c0)) * part_stride(a.G);
-      M = fmaxf(M, rec[g]);
+  // CTA c0's part is its second record, those after it have theirs first
+  auto record = [&](int c) {
+    return a.part + (int64_t(c) * 2 + (c == c0)) * part_stride(a.G);
+  };
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += kJoinParts) {
+    const int k = min(kJoinParts, c1 + 1 - c);
+    // every warp forms the pass's maximum and sum (lane: parts lane, + 32)
+    float mp[2], lp[2];
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = lane + 32 * i;
+      mp[i] = j < k ? record(c + j)[g] : -INFINITY;
+      lp[i] = j < k ? record(c + j)[a.G + g] : 0.f;
+      mx = fmaxf(mx, mp[i]);
     }
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f, acc = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      if (share(total, C, c) == share(total, C, c + 1)) continue;
-      const float* rec =
-          a.part + (int64_t(c) * 2 + (c == c0)) * part_stride(a.G);
-      const float w = exp2f(rec[g] - mu);
-      l += rec[a.G + g] * w;
-      acc += rec[2 * a.G + g * kHeadDim + t] * w;
+    mx = warp_max(mx);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    const float old = exp2f(m - mu);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float w = exp2f(mp[i] - mu);
+      sum += lp[i] * w;
+      if (warp == 0) wt[lane + 32 * i] = w;
     }
-    static_cast<__nv_bfloat16*>(a.out)[(o0 + g) * kHeadDim + t] =
-        __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
-    if (t == 0) a.lse[o0 + g] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * old + sum;
+    m = mx;
+    acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+    __syncthreads();
+    for (int j = warp; j < k; j += kJoinGroups) {
+      const float w = wt[j];
+      const float4 x = reinterpret_cast<const float4*>(
+          record(c + j) + part_acc(a.G) + g * kHeadDim)[lane];
+      acc.x = fmaf(x.x, w, acc.x);
+      acc.y = fmaf(x.y, w, acc.y);
+      acc.z = fmaf(x.z, w, acc.z);
+      acc.w = fmaf(x.w, w, acc.w);
+    }
+    __syncthreads();
   }
+  part[warp][lane] = acc;
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinGroups; ++i) {
+    const float4 x = part[i][lane];
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(out)[lane] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                 pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0)
+    a.lse[blockIdx.x] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -850,8 +903,8 @@ cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
       a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;
   note_launch();
-  e = launch_dependent(kv8_combine_kernel, dim3(a.B * a.H), dim3(kHeadDim), 0,
-                       st, a, C);
+  e = launch_dependent(kv8_combine_kernel, dim3(a.B * a.H * a.G),
+                       dim3(kJoinThreads), 0, st, a, C);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
