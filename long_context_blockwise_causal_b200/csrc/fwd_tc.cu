@@ -911,6 +911,24 @@ bool make_2d_map_strided(CUtensorMap* m, const void* base, int64_t rows,
   return r == CUDA_SUCCESS;
 }
 
+bool make_tokens_map(CUtensorMap* m, const void* base, int B, int T, int H) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {cuuint64_t(kHeadDim), cuuint64_t(H), cuuint64_t(T),
+                        cuuint64_t(B)};
+  cuuint64_t strides[3] = {cuuint64_t(kHeadDim) * 2,
+                           cuuint64_t(H) * kHeadDim * 2,
+                           cuuint64_t(T) * H * kHeadDim * 2};
+  cuuint32_t box[4] = {cuuint32_t(kHeadDim), 1, cuuint32_t(kBlock), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_codes_map(CUtensorMap* m, const void* base, int64_t heads, int L) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;

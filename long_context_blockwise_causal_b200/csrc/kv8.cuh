@@ -29,7 +29,8 @@ struct Kv8WriteArgs {
   int max_pos, B, T, H, L;
   bool int8, half;
 };
-cudaError_t launch_kv8_write(const Kv8WriteArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int* status,
+                             cudaStream_t st);
 
 struct Kv8ReadArgs {
   const void* codes[2];

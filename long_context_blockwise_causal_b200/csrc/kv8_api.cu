@@ -39,6 +39,11 @@ int cache_status(int B, int L, int H, int D, int cache_type) {
   return LWM_OK;
 }
 
+// Blocks of 128 slots that T tokens per row can touch, all heads, K and V.
+int64_t tiles_of(int B, int T, int H) {
+  return int64_t(B) * H * 2 * ((int64_t(T) + kKv8Block - 1) / kKv8Block + 1);
+}
+
 int query_status(int Hq, int H, int max_pos, int rope_layout) {
   if (Hq < 0 || max_pos < 0 ||
       (rope_layout != LWM_ROPE_INTERLEAVED && rope_layout != LWM_ROPE_HALF))
@@ -68,10 +73,8 @@ int lwm_kv8_write(const void* k, const void* v, const int32_t* positions,
     return LWM_ERR_INVALID_ARG;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
   if (int64_t(B) * H == 0 || T == 0 || L == 0) return LWM_OK;
-  // one CTA per block, head and tensor: at most 2^31 - 1 of them
-  if (int64_t(B) * H * 2 * (int64_t(T + kKv8Block - 1) / kKv8Block + 1) >=
-      (int64_t(1) << 31))
-    return LWM_ERR_UNSUPPORTED;
+  // blocks of all heads, K and V, are counted in 32 bits
+  if (tiles_of(B, T, H) >= (int64_t(1) << 31)) return LWM_ERR_UNSUPPORTED;
   if (!wide_ok({k, v, rope_table, k_cache, v_cache, k_bounds}) ||
       !words_ok({positions, start, k_scale, v_scale}) ||
       (n_new && !words_ok({n_new})) || max_pos < 1)
@@ -95,7 +98,10 @@ int lwm_kv8_write(const void* k, const void* v, const int32_t* positions,
   a.L = L;
   a.int8 = cache_type == LWM_KV8_INT8;
   a.half = rope_layout == LWM_ROPE_HALF;
-  return cuda_status(launch_kv8_write(a, static_cast<cudaStream_t>(stream)));
+  int* status = status_word();
+  if (!status) return LWM_ERR_CUDA;
+  return cuda_status(
+      launch_kv8_write(a, status, static_cast<cudaStream_t>(stream)));
 }
 
 int lwm_kv8_read(const void* k_cache, const void* v_cache,
@@ -109,6 +115,7 @@ int lwm_kv8_read(const void* k_cache, const void* v_cache,
     return LWM_ERR_INVALID_ARG;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
   if (int64_t(B) * H == 0 || T == 0) return LWM_OK;
+  if (tiles_of(B, T, H) >= (int64_t(1) << 31)) return LWM_ERR_UNSUPPORTED;
   if (!wide_ok({k_rot, v}) || !words_ok({start}) ||
       (L > 0 && !(wide_ok({k_cache, v_cache}) &&
                   words_ok({k_scale, v_scale}))) ||

@@ -9,277 +9,697 @@
 // one, so that equal inputs give equal codes wherever the definition is
 // evaluated. A scale below the smallest normal number becomes 0 (its codes
 // too); a NaN or an infinity among the new values makes the scale NaN.
+#include <algorithm>
+
 #include "kv8.cuh"
+#include "tc_kernels.cuh"
 
 namespace lwm {
 namespace {
 
-constexpr int kWrThreads = 256;
-constexpr int kWrLanes = 16;                       // lanes per token row
-constexpr int kWrRows = kWrThreads / kWrLanes;     // rows per pass
-constexpr int kWrPasses = kKv8Block / kWrRows;
+constexpr float kMaxFinite = 3.402823466e38f;
 
-// One CTA per (row, block touched, head, K or V): 16 lanes share a token,
-// eight channels each, eight tokens per thread; the block stays in
-// registers between the maximum and the encoding, so the input is read
-// once and the codes are written once.
+// New slots of row b: tokens t in [lo - start, hi - start) go to slots
+// [lo, hi); older tokens lie below lo.
+struct NewSlots {
+  int64_t start, lo, hi;
+};
+__device__ __forceinline__ NewSlots new_slots(const Kv8WriteArgs& a, int b) {
+  NewSlots n;
+  n.start = __ldg(a.start + b);
+  const int count = a.n_new ? max(0, min(__ldg(a.n_new + b), a.T)) : a.T;
+  n.lo = n.start > 0 ? n.start : 0;
+  n.hi = min(n.start + count, int64_t(a.L));
+  return n;
+}
+
+// Scale of a block that had s_old and meets amax.
 template <bool kInt8>
-__global__ void __launch_bounds__(kWrThreads)
-kv8_write_kernel(const Kv8WriteArgs a, int blocks_per_row) {
+__device__ __forceinline__ float block_scale(float s_old, float amax) {
+  constexpr float kRq = kInt8 ? 1.f / kInt8Max : 1.f / kE4m3Max;
+  float s = max_nan(s_old, __fmul_rn(amax, kRq));
+  if (s < kTinyScale) s = 0.f;
+  return s <= kMaxFinite ? s : __int_as_float(0x7fffffff);  // NaN
+}
+
+// Two new values to codes; inv = 1 / s, or 0 for codes of 0 whatever x is.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t code2(float x, float y, float inv) {
+  return inv > 0.f ? enc2<kInt8>(__fmul_rn(x, inv), __fmul_rn(y, inv)) : 0u;
+}
+
+// Four codes of a block whose scale grew.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
+  const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
+  return enc2<kInt8>(__fmul_rn(f.x, ratio), __fmul_rn(f.y, ratio)) |
+         (enc2<kInt8>(__fmul_rn(g.x, ratio), __fmul_rn(g.y, ratio)) << 16);
+}
+
+// Bounds of a channel whose codes lie in [lo, hi], in units of s Q / 127.
+template <bool kInt8>
+__device__ __forceinline__ int bound_lo(float lo) {
+  constexpr float kUnit = kInt8 ? 1.f : kInt8Max / kE4m3Max;
+  return max(-127, min(127, __float2int_rd(__fmul_rn(lo, kUnit))));
+}
+template <bool kInt8>
+__device__ __forceinline__ int bound_hi(float hi) {
+  constexpr float kUnit = kInt8 ? 1.f : kInt8Max / kE4m3Max;
+  return max(-127, min(127, __float2int_ru(__fmul_rn(hi, kUnit))));
+}
+
+__device__ __forceinline__ void rotate(float& x, float& y, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  y = __fadd_rn(__fmul_rn(x, s), __fmul_rn(y, c));
+  x = u;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// ------------------------------------------------------------ few tokens
+//
+// A warp per (row, head, K or V, block touched), four channels per lane
+// (two pairs of the rotation: adjacent channels, or channels 64 apart). The
+// tokens are taken twice, for the maximum and for the codes; the usual
+// append of a token that leaves the scale alone reads the token, the scale
+// and 256 bounds and writes 128 codes. Bound by latency.
+constexpr int kFewThreads = 128;
+constexpr int kFewTokens = 16;
+
+template <bool kInt8, bool kHalf>
+__global__ void __launch_bounds__(kFewThreads)
+kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[kWrThreads / 32];
-  __shared__ float bmin[kWrThreads / 32][kHeadDim];
-  __shared__ float bmax[kWrThreads / 32][kHeadDim];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int c = t % kWrLanes, row0 = t / kWrLanes;
-  int64_t e = blockIdx.x;
-  const int which = int(e & 1);
-  e >>= 1;
-  const int h = int(e % a.H);
-  e /= a.H;
-  const int blk_i = int(e % blocks_per_row);
-  const int b = int(e / blocks_per_row);
-  const bool key = which == 0;
+  const int lane = threadIdx.x & 31;
+  int64_t e = blockIdx.x * int64_t(kFewThreads / 32) + (threadIdx.x >> 5);
+  if (e >= items) return;
+  // the second block of a row's tokens comes after all the first ones
+  const int64_t per = int64_t(a.B) * a.H * 2;
+  const int blk_i = int(e / per);
+  e -= blk_i * per;
+  const bool key = (e & 1) == 0;
+  const int64_t bh = e >> 1;
+  const int b = int(bh / a.H), h = int(bh - int64_t(b) * a.H);
 
-  const int64_t start = a.start[b];
-  const int n_new = a.n_new ? max(0, min(a.n_new[b], a.T)) : a.T;
-  // slots [first, end) get the new tokens; older tokens lie below first
-  const int64_t first = start > 0 ? start : 0;
-  const int64_t end = min(start + n_new, int64_t(a.L));
-  const int64_t base = (first / kKv8Block + blk_i) * kKv8Block;
-  if (first >= end || base >= end) return;
-  const int lo_new = int(max(first - base, int64_t(0)));
-  const int hi_new = int(min(end - base, int64_t(kKv8Block)));
-  const bool has_old = lo_new > 0;
-
+  const NewSlots ns = new_slots(a, b);
+  const int64_t base = (ns.lo / kKv8Block + blk_i) * kKv8Block;
+  if (ns.lo >= ns.hi || base >= ns.hi) return;
+  const int lo = int(max(ns.lo - base, int64_t(0)));
+  const int hi = int(min(ns.hi - base, int64_t(kKv8Block)));
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
-  const int64_t bh = int64_t(b) * a.H + h;
-  const int64_t sc_i = bh * nblk + base / kKv8Block;
-  uint8_t* codes = static_cast<uint8_t*>(a.codes[which]) +
+  const int64_t at = bh * nblk + base / kKv8Block;
+  float* scale = (key ? a.scale[0] : a.scale[1]) + at;
+  uint8_t* codes = static_cast<uint8_t*>(key ? a.codes[0] : a.codes[1]) +
                    (bh * a.L + base) * kHeadDim;
-  const float s_old = has_old ? a.scale[which][sc_i] : 0.f;
+  const char* x_all = static_cast<const char*>(key ? a.x[0] : a.x[1]);
+  const float s_old = lo > 0 ? *scale : 0.f;
+  const int c0 = kHalf ? 2 * lane : 4 * lane;        // channels c0, c0 + 1,
+  const int c1 = kHalf ? 64 + 2 * lane : c0 + 2;     // c1, c1 + 1
 
-  float x[kWrPasses][8];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kWrPasses; ++i) {
-    const int r = row0 + i * kWrRows;
-    const bool on = r >= lo_new && r < hi_new;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    int p = 0;
-    if (on) {
-      const int64_t tok = int64_t(b) * a.T + (base + r - start);
-      w = __ldg(reinterpret_cast<const uint4*>(a.x[which]) +
-                (tok * a.H + h) * kWrLanes + c);
-      if (key) p = max(0, min(__ldg(a.positions + tok), a.max_pos - 1));
-    }
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[i][2 * k] = bf16lo_to_f32(ws[k]);
-      x[i][2 * k + 1] = bf16hi_to_f32(ws[k]);
-    }
+  float x[4];
+  auto load = [&](int r) {
+    const int64_t tok = int64_t(b) * a.T + (base + r - ns.start);
+    const char* row = x_all + (tok * a.H + h) * (kHeadDim * 2);
+    const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(row + 2 * c0));
+    const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(row + 2 * c1));
+    x[0] = bf16lo_to_f32(w0);
+    x[1] = bf16hi_to_f32(w0);
+    x[2] = bf16lo_to_f32(w1);
+    x[3] = bf16hi_to_f32(w1);
     if (key) {
-      const float4* tab = reinterpret_cast<const float4*>(
-          a.table + int64_t(p) * kHeadDim);
-      if (a.half) {
-        // channels 8c' .. 8c'+7 pair with those 64 further up, held by the
-        // lane eight away
-        const float4* tc = tab + (c & 7) * 4;
-        const bool low = c < 8;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 cs =
-              on ? __ldg(tc + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float cc[2] = {cs.x, cs.z}, ss[2] = {cs.y, cs.w};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float me = x[i][2 * k + u];
-            const float other = __shfl_xor_sync(0xffffffffu, me, 8);
-            x[i][2 * k + u] =
-                low ? __fsub_rn(__fmul_rn(me, cc[u]), __fmul_rn(other, ss[u]))
-                    : __fadd_rn(__fmul_rn(other, ss[u]), __fmul_rn(me, cc[u]));
-          }
-        }
+      const int p = max(0, min(__ldg(a.positions + tok), a.max_pos - 1));
+      // pairs 2 lane and 2 lane + 1
+      const float4 cs = __ldg(reinterpret_cast<const float4*>(
+                                  a.table + int64_t(p) * kHeadDim) + lane);
+      if (kHalf) {
+        rotate(x[0], x[2], cs.x, cs.y);
+        rotate(x[1], x[3], cs.z, cs.w);
       } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float4 cs =
-              on ? __ldg(tab + c * 2 + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float cc[2] = {cs.x, cs.z}, ss[2] = {cs.y, cs.w};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float p0 = x[i][4 * k + 2 * u], p1 = x[i][4 * k + 2 * u + 1];
-            x[i][4 * k + 2 * u] =
-                __fsub_rn(__fmul_rn(p0, cc[u]), __fmul_rn(p1, ss[u]));
-            x[i][4 * k + 2 * u + 1] =
-                __fadd_rn(__fmul_rn(p0, ss[u]), __fmul_rn(p1, cc[u]));
-          }
-        }
+        rotate(x[0], x[1], cs.x, cs.y);
+        rotate(x[2], x[3], cs.z, cs.w);
       }
     }
+  };
+  float mn[4], mx[4], amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) amax = max_nan(amax, fabsf(x[i][k]));
+  for (int k = 0; k < 4; ++k) {
+    mn[k] = INFINITY;
+    mx[k] = -INFINITY;
+  }
+  for (int r = lo; r < hi; ++r) {
+    load(r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      mn[k] = min_nan(mn[k], x[k]);
+      mx[k] = max_nan(mx[k], x[k]);
+      amax = max_nan(amax, fabsf(x[k]));
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) red[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kWrThreads / 32; ++k) amax = max_nan(amax, red[k]);
-
-  constexpr float kRq = kInt8 ? 1.f / kInt8Max : 1.f / kE4m3Max;
-  float s = max_nan(s_old, __fmul_rn(amax, kRq));
-  if (s < kTinyScale) s = 0.f;
-  if (!(s <= 3.402823466e38f)) s = __int_as_float(0x7fffffff);  // NaN
-  const bool ok = s > 0.f;                        // false for NaN
-  const float inv = ok ? __fdiv_rn(1.f, s) : 0.f;
-  // older codes change only when the scale grew; a NaN leaves them
-  const bool grew = has_old && ok && s > s_old;
-  const float ratio = grew ? __fdiv_rn(s_old, s) : 1.f;
-
-  float mn[8], mx[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    mn[k] = INFINITY;
-    mx[k] = -INFINITY;
-  }
-#pragma unroll
-  for (int i = 0; i < kWrPasses; ++i) {
-    const int r = row0 + i * kWrRows;
-    uint2* at = reinterpret_cast<uint2*>(codes + r * kHeadDim + c * 8);
-    const bool is_new = r >= lo_new && r < hi_new;
-    if (!is_new && !(grew && r < lo_new)) continue;
-    uint32_t w[4];
-    if (is_new) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = ok ? enc2<kInt8>(__fmul_rn(x[i][2 * k], inv),
-                                __fmul_rn(x[i][2 * k + 1], inv))
-                  : 0u;
+  const float s = block_scale<kInt8>(s_old, amax);
+  const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+  const bool grew = lo > 0 && s > s_old;
+  for (int r = lo; r < hi; ++r) {
+    if (hi - lo > 1) load(r);
+    uint8_t* row = codes + r * kHeadDim;
+    const uint32_t w0 = code2<kInt8>(x[0], x[1], inv);
+    const uint32_t w1 = code2<kInt8>(x[2], x[3], inv);
+    if (kHalf) {
+      *reinterpret_cast<uint16_t*>(row + c0) = uint16_t(w0);
+      *reinterpret_cast<uint16_t*>(row + c1) = uint16_t(w1);
     } else {
-      const uint2 old = *at;
-      const uint32_t ow[4] = {old.x & 0xffffu, old.x >> 16, old.y & 0xffffu,
-                              old.y >> 16};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = dec2<kInt8>(ow[k]);
-        w[k] = enc2<kInt8>(__fmul_rn(f.x, ratio), __fmul_rn(f.y, ratio));
-      }
-    }
-    *at = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    if (key) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = dec2<kInt8>(w[k]);
-        mn[2 * k] = fminf(mn[2 * k], f.x);
-        mx[2 * k] = fmaxf(mx[2 * k], f.x);
-        mn[2 * k + 1] = fminf(mn[2 * k + 1], f.y);
-        mx[2 * k + 1] = fmaxf(mx[2 * k + 1], f.y);
-      }
+      *reinterpret_cast<uint32_t*>(row + c0) = w0 | (w1 << 16);
     }
   }
-  if (t == 0) a.scale[which][sc_i] = s;
+  if (lane == 0) *scale = s;
+  // the new codes' range: encoding keeps the order
+  float cl[4], ch[4];
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const float2 f = dec2<kInt8>(code2<kInt8>(mn[k], mn[k + 1], inv));
+    const float2 g = dec2<kInt8>(code2<kInt8>(mx[k], mx[k + 1], inv));
+    cl[k] = f.x; cl[k + 1] = f.y;
+    ch[k] = g.x; ch[k + 1] = g.y;
+  }
+  if (grew) {
+    // round the older codes again; a lane takes its own four channels of
+    // every row, so it also has their range
+    const float ratio = __fdiv_rn(s_old, s);
+#pragma unroll 4
+    for (int r = 0; r < lo; ++r) {
+      uint8_t* row = codes + r * kHeadDim;
+      uint32_t w;
+      if (kHalf) {
+        w = *reinterpret_cast<const uint16_t*>(row + c0) |
+            (uint32_t(*reinterpret_cast<const uint16_t*>(row + c1)) << 16);
+      } else {
+        w = *reinterpret_cast<const uint32_t*>(row + c0);
+      }
+      w = recode4<kInt8>(w, ratio);
+      if (kHalf) {
+        *reinterpret_cast<uint16_t*>(row + c0) = uint16_t(w);
+        *reinterpret_cast<uint16_t*>(row + c1) = uint16_t(w >> 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(row + c0) = w;
+      }
+      const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
+      cl[0] = fminf(cl[0], f.x); ch[0] = fmaxf(ch[0], f.x);
+      cl[1] = fminf(cl[1], f.y); ch[1] = fmaxf(ch[1], f.y);
+      cl[2] = fminf(cl[2], g.x); ch[2] = fmaxf(ch[2], g.x);
+      cl[3] = fminf(cl[3], g.y); ch[3] = fmaxf(ch[3], g.y);
+    }
+  }
   if (!key) return;
+  int8_t* bd = a.k_bounds + at * 2 * kHeadDim;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 16));
-    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 16));
-  }
-  if (lane < kWrLanes) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      bmin[warp][c * 8 + k] = mn[k];
-      bmax[warp][c * 8 + k] = mx[k];
+  for (int k = 0; k < 4; k += 2) {
+    char2* pl = reinterpret_cast<char2*>(bd + (k ? c1 : c0));
+    char2* ph = reinterpret_cast<char2*>(bd + kHeadDim + (k ? c1 : c0));
+    int l0 = bound_lo<kInt8>(cl[k]), l1 = bound_lo<kInt8>(cl[k + 1]);
+    int h0 = bound_hi<kInt8>(ch[k]), h1 = bound_hi<kInt8>(ch[k + 1]);
+    if (lo > 0 && !grew) {     // the older tokens' bounds still hold
+      const char2 ol = *pl, oh = *ph;
+      l0 = min(l0, int(ol.x)); l1 = min(l1, int(ol.y));
+      h0 = max(h0, int(oh.x)); h1 = max(h1, int(oh.y));
     }
-  }
-  __syncthreads();
-  if (t < kHeadDim) {
-    float m0 = INFINITY, m1 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWrThreads / 32; ++w) {
-      m0 = fminf(m0, bmin[w][t]);
-      m1 = fmaxf(m1, bmax[w][t]);
-    }
-    constexpr float kUnit = kInt8 ? 1.f : kInt8Max / kE4m3Max;
-    int lo = __float2int_rd(__fmul_rn(m0, kUnit));
-    int hi = __float2int_ru(__fmul_rn(m1, kUnit));
-    lo = max(-127, min(127, lo));
-    hi = max(-127, min(127, hi));
-    int8_t* bd = a.k_bounds + sc_i * 2 * kHeadDim;
-    if (has_old && !grew) {  // the older tokens' bounds still hold
-      lo = min(lo, int(bd[t]));
-      hi = max(hi, int(bd[kHeadDim + t]));
-    }
-    bd[t] = int8_t(lo);
-    bd[kHeadDim + t] = int8_t(hi);
+    *pl = make_char2(char(l0), char(l1));
+    *ph = make_char2(char(h0), char(h1));
   }
 }
 
-// out[b][t][h] = code * scale of slot start[b] + t, zeros outside
-// [0, min(kv_len[b], L)). Eight lanes per row of 128 codes, 16 codes each.
-template <bool kInt8>
-__global__ void kv8_read_kernel(const Kv8ReadArgs a) {
+// ----------------------------------------------------------- many tokens
+//
+// A CTA takes a block of 128 slots of K or V for a group of heads, one head
+// after the other: the heads' [128 tokens][128] bf16 boxes come in by TMA
+// through a ring of stages, while the rotation's angles of the block's
+// tokens stay in registers. 16 lanes share a token, eight channels each,
+// four tokens per thread; the rotated block stays in registers between the
+// maximum and the encoding, so each input is read once and each code
+// written once. K keeps the channels' smallest and largest value, which
+// give the block's maximum as well as its bounds. One barrier per head.
+constexpr int kWrThreads = 512;
+constexpr int kWrWarps = kWrThreads / 32;
+constexpr int kWrLanes = 16;
+constexpr int kWrStep = kWrThreads / kWrLanes;     // tokens per pass
+constexpr int kWrPasses = kKv8Block / kWrStep;
+constexpr int kWrStages = 4;
+constexpr int kWrTile = kKv8Block * kHeadDim * 2;
+constexpr uint64_t kWrWaitNs = 4000000000ull;
+// shared memory (bytes): stages, channel ranges [2][lo, hi][warp][128],
+// maxima [2][warp], barriers
+constexpr int kWrChan = kWrStages * kWrTile;
+constexpr int kWrMax = kWrChan + 2 * 2 * kWrWarps * kHeadDim * 4;
+constexpr int kWrBars = kWrMax + 2 * kWrWarps * 4;
+constexpr int kWrSmem = kWrBars + kWrStages * 8 + 128;
+static_assert(kWrSmem <= 232448, "shared memory per CTA");
+
+struct WriteItem {
+  int b, h0, h1;
+  bool key;
+  int64_t base;       // first slot of the block
+  int lo, hi;         // its new slots
+  int64_t tok;        // token of the block's first slot (may be negative)
+  bool any;
+};
+
+struct WriteGrid {
+  int per_row;        // blocks a row's tokens can touch
+  int groups, heads;  // head groups and heads in each
+  int64_t items;      // 2 * B * per_row * groups
+};
+
+__device__ __forceinline__ WriteItem write_item(const Kv8WriteArgs& a,
+                                                const WriteGrid& g,
+                                                int64_t i) {
+  WriteItem w;
+  // all of K, then all of V; within each, heads of a block side by side
+  const int64_t half = g.items / 2;
+  w.key = i < half;
+  if (!w.key) i -= half;
+  const int64_t row_blk = i / g.groups;
+  w.h0 = int(i - row_blk * g.groups) * g.heads;
+  w.h1 = min(w.h0 + g.heads, a.H);
+  w.b = int(row_blk / g.per_row);
+  const NewSlots n = new_slots(a, w.b);
+  w.base = (n.lo / kKv8Block + (row_blk - int64_t(w.b) * g.per_row)) *
+           kKv8Block;
+  w.any = n.lo < n.hi && w.base < n.hi;
+  w.lo = int(max(n.lo - w.base, int64_t(0)));
+  w.hi = int(min(n.hi - w.base, int64_t(kKv8Block)));
+  w.tok = w.base - n.start;
+  return w;
+}
+
+template <bool kInt8, bool kHalf>
+__global__ void __launch_bounds__(kWrThreads, 1)
+kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ Kv8WriteArgs a,
+                 const WriteGrid grid, int* status) {
+  extern __shared__ uint8_t dsmem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~uintptr_t(127));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int s) { return sbase + kWrBars + 8u * s; };
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int c = t % kWrLanes, row0 = t / kWrLanes;
+  if (t == 0) {
+    for (int s = 0; s < kWrStages; ++s) mbar_init(bar(s), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int which = blockIdx.y;
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
-  const int64_t n = int64_t(a.B) * a.T * a.H * 8;
-  for (int64_t e = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; e < n;
-       e += int64_t(gridDim.x) * blockDim.x) {
-    const int c = int(e & 7);
-    const int64_t row = e >> 3;              // (b, t, h)
-    const int h = int(row % a.H);
-    const int64_t bt = row / a.H;
-    const int b = int(bt / a.T);
-    const int64_t slot = int64_t(__ldg(a.start + b)) + (bt - int64_t(b) * a.T);
-    const int len = a.kv_len ? min(__ldg(a.kv_len + b), a.L) : a.L;
-    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (slot >= 0 && slot < len) {
-      const int64_t bh = int64_t(b) * a.H + h;
-      const float s = __ldg(a.scale[which] + bh * nblk + slot / kKv8Block);
-      const uint4 w = __ldg(
-          reinterpret_cast<const uint4*>(a.codes[which]) +
-          (bh * a.L + slot) * 8 + c);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+
+  // loader (thread 0): runs kWrStages - 1 heads ahead over the same items
+  int64_t ld_i = blockIdx.x;
+  WriteItem ld{};
+  int ld_h = 0, ld_n = 0;
+  auto ld_seek = [&]() {
+    while (ld_i < grid.items) {
+      ld = write_item(a, grid, ld_i);
+      ld_h = ld.h0;
+      if (ld.any) return;
+      ld_i += gridDim.x;
+    }
+  };
+  auto ld_issue = [&]() {
+    if (ld_i >= grid.items) return;
+    const int s = ld_n % kWrStages;
+    mbar_arrive_expect_tx(bar(s), kWrTile);
+    // tokens before the first and behind the last one read as zeros
+    tma_load_4d(sbase + s * kWrTile, ld.key ? &tm_k : &tm_v, bar(s), 0, ld_h,
+                int(ld.tok), ld.b);
+    ++ld_n;
+    if (++ld_h >= ld.h1) {
+      ld_i += gridDim.x;
+      ld_seek();
+    }
+  };
+  if (t == 0) {
+    ld_seek();
+    for (int s = 0; s < kWrStages - 1; ++s) ld_issue();
+  }
+
+  int n = 0;          // heads done
+  for (int64_t i = blockIdx.x; i < grid.items; i += gridDim.x) {
+    const WriteItem it = write_item(a, grid, i);
+    if (!it.any) continue;
+    // angles of the thread's tokens, pairs 4c .. 4c + 3
+    float4 cs[kWrPasses][2];
+    if (it.key) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f0 = dec2<kInt8>(ws[k] & 0xffffu);
-        const float2 f1 = dec2<kInt8>(ws[k] >> 16);
-        o[2 * k] = pack_bf16x2(f0.x * s, f0.y * s);
-        o[2 * k + 1] = pack_bf16x2(f1.x * s, f1.y * s);
+      for (int k = 0; k < kWrPasses; ++k) {
+        const int r = row0 + k * kWrStep;
+        int p = 0;
+        if (r >= it.lo && r < it.hi)
+          p = max(0, min(__ldg(a.positions + int64_t(it.b) * a.T + it.tok + r),
+                         a.max_pos - 1));
+        const float4* tab = reinterpret_cast<const float4*>(
+            a.table + int64_t(p) * kHeadDim) + 2 * c;
+        cs[k][0] = __ldg(tab);
+        cs[k][1] = __ldg(tab + 1);
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>(a.out[which]) + e * 2;
+    for (int h = it.h0; h < it.h1; ++h, ++n) {
+      const int64_t bh = int64_t(it.b) * a.H + h;
+      const int64_t at = bh * nblk + it.base / kKv8Block;
+      float* scale = (it.key ? a.scale[0] : a.scale[1]) + at;
+      const float s_old = it.lo > 0 ? __ldcg(scale) : 0.f;
+      const bool ok = mbar_wait(bar(n % kWrStages), (n / kWrStages) & 1,
+                                nullptr, status, kWrWaitNs);
+      const uint8_t* tile = smem + (n % kWrStages) * kWrTile;
+      float x[kWrPasses][8];
+#pragma unroll
+      for (int k = 0; k < kWrPasses; ++k) {
+        const uint8_t* row = tile + (row0 + k * kWrStep) * (kHeadDim * 2);
+        uint32_t w[4];
+        if (kHalf) {
+          const uint2 u = *reinterpret_cast<const uint2*>(row + c * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(row + 128 + c * 8);
+          w[0] = u.x; w[1] = u.y; w[2] = v.x; w[3] = v.y;
+        } else {
+          const uint4 u = *reinterpret_cast<const uint4*>(row + c * 16);
+          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[k][2 * j] = bf16lo_to_f32(w[j]);
+          x[k][2 * j + 1] = bf16hi_to_f32(w[j]);
+        }
+      }
+      float mn[8], mx[8], amax = 0.f;
+      if (it.key) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          mn[j] = INFINITY;
+          mx[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < kWrPasses; ++k) {
+          const float4 q0 = cs[k][0], q1 = cs[k][1];
+          if (kHalf) {
+            rotate(x[k][0], x[k][4], q0.x, q0.y);
+            rotate(x[k][1], x[k][5], q0.z, q0.w);
+            rotate(x[k][2], x[k][6], q1.x, q1.y);
+            rotate(x[k][3], x[k][7], q1.z, q1.w);
+          } else {
+            rotate(x[k][0], x[k][1], q0.x, q0.y);
+            rotate(x[k][2], x[k][3], q0.z, q0.w);
+            rotate(x[k][4], x[k][5], q1.x, q1.y);
+            rotate(x[k][6], x[k][7], q1.z, q1.w);
+          }
+          const int r = row0 + k * kWrStep;
+          if (r >= it.lo && r < it.hi) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              mn[j] = min_nan(mn[j], x[k][j]);
+              mx[j] = max_nan(mx[j], x[k][j]);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          mn[j] = min_nan(mn[j], __shfl_xor_sync(0xffffffffu, mn[j], 16));
+          mx[j] = max_nan(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
+        }
+        float* chan = reinterpret_cast<float*>(smem + kWrChan) +
+                      ((n & 1) * 2 * kWrWarps + warp) * kHeadDim;
+        if (lane < kWrLanes) {
+          // interleaved: channels 8c ..; half: 4c .. and 64 + 4c ..
+          float* lo4 = chan + (kHalf ? 4 * c : 8 * c);
+          float* hi4 = kHalf ? lo4 + 64 : lo4 + 4;
+          *reinterpret_cast<float4*>(lo4) =
+              make_float4(mn[0], mn[1], mn[2], mn[3]);
+          *reinterpret_cast<float4*>(hi4) =
+              make_float4(mn[4], mn[5], mn[6], mn[7]);
+          *reinterpret_cast<float4*>(lo4 + kWrWarps * kHeadDim) =
+              make_float4(mx[0], mx[1], mx[2], mx[3]);
+          *reinterpret_cast<float4*>(hi4 + kWrWarps * kHeadDim) =
+              make_float4(mx[4], mx[5], mx[6], mx[7]);
+        }
+        // a warp none of whose tokens is new has mn > mx
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!(mn[j] > mx[j]))
+            amax = max_nan(amax, max_nan(fabsf(mn[j]), fabsf(mx[j])));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kWrPasses; ++k) {
+          const int r = row0 + k * kWrStep;
+          if (r >= it.lo && r < it.hi) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[k][j]));
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float* red = reinterpret_cast<float*>(smem + kWrMax) +
+                   (n & 1) * kWrWarps;
+      if (lane == 0) red[warp] = amax;
+      // all have read the tile: its stage is free
+      if (!__syncthreads_and(ok)) {
+        // a load did not land in time: wait for the others before leaving
+        if (t == 0)
+          for (int f = n + 1; f < ld_n; ++f)
+            mbar_wait(bar(f % kWrStages), (f / kWrStages) & 1, nullptr,
+                      status, kWrWaitNs);
+        return;
+      }
+      if (t == 0) ld_issue();
+#pragma unroll
+      for (int w = 0; w < kWrWarps; w += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(red + w);
+        amax = max_nan(amax, max_nan(max_nan(m4.x, m4.y), max_nan(m4.z, m4.w)));
+      }
+      const float s = block_scale<kInt8>(s_old, amax);
+      const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+      const bool grew = it.lo > 0 && s > s_old;
+      uint8_t* codes = static_cast<uint8_t*>(it.key ? a.codes[0] : a.codes[1]) +
+                       (bh * a.L + it.base) * kHeadDim;
+#pragma unroll
+      for (int k = 0; k < kWrPasses; ++k) {
+        const int r = row0 + k * kWrStep;
+        if (r < it.lo || r >= it.hi) continue;
+        const uint32_t w0 = code2<kInt8>(x[k][0], x[k][1], inv) |
+                            (code2<kInt8>(x[k][2], x[k][3], inv) << 16);
+        const uint32_t w1 = code2<kInt8>(x[k][4], x[k][5], inv) |
+                            (code2<kInt8>(x[k][6], x[k][7], inv) << 16);
+        uint8_t* row = codes + r * kHeadDim;
+        if (kHalf) {
+          *reinterpret_cast<uint32_t*>(row + c * 4) = w0;
+          *reinterpret_cast<uint32_t*>(row + 64 + c * 4) = w1;
+        } else {
+          *reinterpret_cast<uint2*>(row + c * 8) = make_uint2(w0, w1);
+        }
+      }
+      if (t == 0) *scale = s;
+      if (grew) {
+        // the block's older codes, rounded again: four channels per thread
+        const float ratio = __fdiv_rn(s_old, s);
+        const int c4 = (t & 31) * 4;
+        float lo4[4], hi4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lo4[j] = INFINITY;
+          hi4[j] = -INFINITY;
+        }
+        for (int r = warp; r < it.lo; r += kWrWarps) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(codes + r * kHeadDim + c4);
+          const uint32_t w = recode4<kInt8>(*p, ratio);
+          *p = w;
+          const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
+          const float v[4] = {f.x, f.y, g.x, g.y};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            lo4[j] = fminf(lo4[j], v[j]);
+            hi4[j] = fmaxf(hi4[j], v[j]);
+          }
+        }
+        if (it.key) {
+          // through the other half of the channel ranges
+          float* chan = reinterpret_cast<float*>(smem + kWrChan) +
+                        (((n & 1) ^ 1) * 2 * kWrWarps + warp) * kHeadDim + c4;
+          *reinterpret_cast<float4*>(chan) =
+              make_float4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          *reinterpret_cast<float4*>(chan + kWrWarps * kHeadDim) =
+              make_float4(hi4[0], hi4[1], hi4[2], hi4[3]);
+          __syncthreads();
+        }
+      }
+      if (it.key && t < kHeadDim) {
+        const float* chan = reinterpret_cast<const float*>(smem + kWrChan) +
+                            (n & 1) * 2 * kWrWarps * kHeadDim + t;
+        float m0 = INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWrWarps; ++w) {
+          m0 = fminf(m0, chan[w * kHeadDim]);
+          m1 = fmaxf(m1, chan[(kWrWarps + w) * kHeadDim]);
+        }
+        // encoding keeps the order
+        const float2 f = dec2<kInt8>(code2<kInt8>(m0, m1, inv));
+        float lo = f.x, hi = f.y;
+        if (grew) {
+          const float* old = reinterpret_cast<const float*>(smem + kWrChan) +
+                             ((n & 1) ^ 1) * 2 * kWrWarps * kHeadDim + t;
+#pragma unroll
+          for (int w = 0; w < kWrWarps; ++w) {
+            lo = fminf(lo, old[w * kHeadDim]);
+            hi = fmaxf(hi, old[(kWrWarps + w) * kHeadDim]);
+          }
+        }
+        int l = bound_lo<kInt8>(lo), u = bound_hi<kInt8>(hi);
+        int8_t* bd = a.k_bounds + at * 2 * kHeadDim;
+        if (it.lo > 0 && !grew) {   // the older tokens' bounds still hold
+          l = min(l, int(bd[t]));
+          u = max(u, int(bd[kHeadDim + t]));
+        }
+        bd[t] = int8_t(l);
+        bd[kHeadDim + t] = int8_t(u);
+      }
+      if (grew && it.key) __syncthreads();   // the ranges have been read
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read
+//
+// out[b][t][h] = code * scale of slot start[b] + t, zeros outside
+// [0, min(kv_len[b], L)). A CTA takes 128 tokens of one (row, head) of K or
+// V: eight lanes per row of 128 codes, 16 codes each, four rows per thread
+// with their loads in flight together. Heads are neighbours in the grid,
+// so that a token's heads, adjacent in the output, are written close in
+// time.
+constexpr int kRdThreads = 256;
+constexpr int kRdRows = kRdThreads / 8;
+constexpr int kRdPasses = 4;
+constexpr int kRdTokens = kRdRows * kRdPasses;
+
+template <bool kInt8>
+__global__ void __launch_bounds__(kRdThreads)
+kv8_read_kernel(const __grid_constant__ Kv8ReadArgs a, int tiles) {
+  pdl_wait();
+  pdl_trigger();
+  uint32_t e = blockIdx.x;
+  const bool key = (e & 1) == 0;
+  e >>= 1;
+  const int h = int(e % uint32_t(a.H));
+  e /= uint32_t(a.H);
+  const int b = int(e / uint32_t(tiles));
+  const int t0 = int(e - uint32_t(b) * uint32_t(tiles)) * kRdTokens;
+  const int c = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
+  const int64_t bh = int64_t(b) * a.H + h;
+  const int64_t start = __ldg(a.start + b);
+  const int len = a.kv_len ? min(__ldg(a.kv_len + b), a.L) : a.L;
+  const uint4* codes =
+      static_cast<const uint4*>(key ? a.codes[0] : a.codes[1]) +
+      bh * a.L * 8 + c;
+  const float* scale = (key ? a.scale[0] : a.scale[1]) + bh * nblk;
+  uint4 w[kRdPasses];
+  float s[kRdPasses];
+#pragma unroll
+  for (int i = 0; i < kRdPasses; ++i) {
+    const int tok = t0 + row + i * kRdRows;
+    const int64_t slot = start + tok;
+    w[i] = make_uint4(0, 0, 0, 0);
+    s[i] = 0.f;
+    if (tok < a.T && slot >= 0 && slot < len) {
+      w[i] = __ldg(codes + slot * 8);
+      s[i] = __ldg(scale + slot / kKv8Block);
+    }
+  }
+  uint4* out = static_cast<uint4*>(key ? a.out[0] : a.out[1]) + c * 2;
+#pragma unroll
+  for (int i = 0; i < kRdPasses; ++i) {
+    const int tok = t0 + row + i * kRdRows;
+    if (tok >= a.T) continue;
+    const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f0 = dec2<kInt8>(ws[k] & 0xffffu);
+      const float2 f1 = dec2<kInt8>(ws[k] >> 16);
+      o[2 * k] = pack_bf16x2(f0.x * s[i], f0.y * s[i]);
+      o[2 * k + 1] = pack_bf16x2(f1.x * s[i], f1.y * s[i]);
+    }
+    uint4* dst = out + ((int64_t(b) * a.T + tok) * a.H + h) * 16;
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
+template <bool kInt8, bool kHalf>
+cudaError_t launch_few(const Kv8WriteArgs& a, cudaStream_t st) {
+  const int64_t items = int64_t(a.B) * a.H * 2 * (a.T > 1 ? 2 : 1);
+  const int64_t grid = (items + kFewThreads / 32 - 1) / (kFewThreads / 32);
+  return launch_dependent(kv8_write_few_kernel<kInt8, kHalf>,
+                          dim3(unsigned(grid)), dim3(kFewThreads), 0, st, a,
+                          items);
+}
+
+template <bool kInt8, bool kHalf>
+cudaError_t launch_many(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!make_tokens_map(&mk, a.x[0], a.B, a.T, a.H) ||
+      !make_tokens_map(&mv, a.x[1], a.B, a.T, a.H))
+    return cudaErrorInvalidValue;
+  const int sms = sm_count();
+  WriteGrid g{};
+  g.per_row = (a.T + kKv8Block - 1) / kKv8Block + 1;
+  // as many heads per item as leave each SM four items or more: a longer
+  // run reuses the angles, a shorter one spreads the work
+  const int64_t tiles = 2 * int64_t(a.B) * g.per_row * a.H;
+  g.heads = int(std::max<int64_t>(
+      1, std::min<int64_t>({16, tiles / (4 * sms), a.H})));
+  g.groups = (a.H + g.heads - 1) / g.heads;
+  g.items = 2 * int64_t(a.B) * g.per_row * g.groups;
+  cudaError_t e = cudaFuncSetAttribute(
+      kv8_write_kernel<kInt8, kHalf>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kWrSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(g.items, sms);
+  return launch_dependent(kv8_write_kernel<kInt8, kHalf>,
+                          dim3(unsigned(ctas)), dim3(kWrThreads), kWrSmem, st,
+                          mk, mv, a, g, status);
+}
+
+template <bool kInt8, bool kHalf>
+cudaError_t launch_write(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
+  return a.T <= kFewTokens ? launch_few<kInt8, kHalf>(a, st)
+                           : launch_many<kInt8, kHalf>(a, status, st);
+}
+
 }  // namespace
 
-cudaError_t launch_kv8_write(const Kv8WriteArgs& a, cudaStream_t st) {
-  const int per_row = (a.T + kKv8Block - 1) / kKv8Block + 1;
-  const int64_t grid = int64_t(a.B) * per_row * a.H * 2;
-  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_dependent(
-      a.int8 ? kv8_write_kernel<true> : kv8_write_kernel<false>,
-      dim3(unsigned(grid)), dim3(kWrThreads), 0, st, a, per_row);
+cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int* status,
+                             cudaStream_t st) {
+  const cudaError_t e =
+      a.int8 ? (a.half ? launch_write<true, true>(a, status, st)
+                       : launch_write<true, false>(a, status, st))
+             : (a.half ? launch_write<false, true>(a, status, st)
+                       : launch_write<false, false>(a, status, st));
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv8_read(const Kv8ReadArgs& a, cudaStream_t st) {
-  const int64_t n = int64_t(a.B) * a.T * a.H * 8;
-  const int threads = 256;
-  const int64_t want = (n + threads - 1) / threads;
-  const unsigned grid = unsigned(want < (1 << 20) ? want : (1 << 20));
+  const int tiles = (a.T + kRdTokens - 1) / kRdTokens;
+  const int64_t grid = int64_t(a.B) * a.H * tiles * 2;
   const cudaError_t e = launch_dependent(
-      a.int8 ? kv8_read_kernel<true> : kv8_read_kernel<false>, dim3(grid, 2),
-      dim3(threads), 0, st, a);
+      a.int8 ? kv8_read_kernel<true> : kv8_read_kernel<false>,
+      dim3(unsigned(grid)), dim3(kRdThreads), 0, st, a, tiles);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();

@@ -96,6 +96,9 @@ bool make_2d_map_strided(CUtensorMap* m, const void* base, int64_t rows,
 // Codes of an 8-bit cache, bytes [heads][L][128], as a 3-D map; box 128
 // bytes x 128 rows x 1 with the 128-byte swizzle. Rows past L read as 0.
 bool make_codes_map(CUtensorMap* m, const void* base, int64_t heads, int L);
+// New tokens, bf16 [B][T][H][128], as a 4-D map {128, H, T, B}; box 128
+// channels x 1 head x 128 tokens, no swizzle (rows of 256 bytes).
+bool make_tokens_map(CUtensorMap* m, const void* base, int B, int T, int H);
 int sm_count();
 cudaError_t launch_bwd_tc(const BwdArgs& a, cudaStream_t st);
 
