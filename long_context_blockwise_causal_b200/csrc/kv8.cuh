@@ -119,11 +119,67 @@ template <bool kInt8>
 __device__ __forceinline__ float2 dec2(uint32_t w) {
   return kInt8 ? dec2_int8(w) : dec2_e4m3(w);
 }
+// Four values to codes in one word. int8: |v| is at most 127 but for the
+// last bit of a product, so adding 1.5 * 2^23 rounds it to nearest even and
+// leaves the code in the low byte, with nothing to clamp.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
+  if constexpr (kInt8) {
+    constexpr float kMagic = 12582912.f;
+    const uint32_t ua = __float_as_uint(__fadd_rn(a, kMagic));
+    const uint32_t ub = __float_as_uint(__fadd_rn(b, kMagic));
+    const uint32_t uc = __float_as_uint(__fadd_rn(c, kMagic));
+    const uint32_t ud = __float_as_uint(__fadd_rn(d, kMagic));
+    return __byte_perm(__byte_perm(ua, ub, 0x0040),
+                       __byte_perm(uc, ud, 0x0040), 0x5410);
+  } else {
+    return enc2_e4m3(a, b) | (enc2_e4m3(c, d) << 16);
+  }
+}
+// Packed products and sums, each rounded once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return fma2(b, make_float2(-1.f, -1.f), a);   // the product is exact
+}
 // max that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Largest of a warp's magnitudes (no sign bit); as unsigned words their
+// order is the numbers', with NaN on top.
+__device__ __forceinline__ float warp_max_abs(float x) {
+  return __uint_as_float(
+      __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x))));
 }
 #endif
 

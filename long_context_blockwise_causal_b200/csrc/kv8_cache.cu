@@ -52,8 +52,8 @@ __device__ __forceinline__ uint32_t code2(float x, float y, float inv) {
 template <bool kInt8>
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
-  return enc2<kInt8>(__fmul_rn(f.x, ratio), __fmul_rn(f.y, ratio)) |
-         (enc2<kInt8>(__fmul_rn(g.x, ratio), __fmul_rn(g.y, ratio)) << 16);
+  return enc4<kInt8>(__fmul_rn(f.x, ratio), __fmul_rn(f.y, ratio),
+                     __fmul_rn(g.x, ratio), __fmul_rn(g.y, ratio));
 }
 
 // Bounds of a channel whose codes lie in [lo, hi], in units of s Q / 127.
@@ -72,12 +72,6 @@ __device__ __forceinline__ void rotate(float& x, float& y, float c, float s) {
   const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
   y = __fadd_rn(__fmul_rn(x, s), __fmul_rn(y, c));
   x = u;
-}
-
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
 }
 
 // ------------------------------------------------------------ few tokens
@@ -160,9 +154,7 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
       amax = max_nan(amax, fabsf(x[k]));
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  amax = warp_max_abs(amax);
   const float s = block_scale<kInt8>(s_old, amax);
   const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
   const bool grew = lo > 0 && s > s_old;
@@ -189,31 +181,41 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
     ch[k] = g.x; ch[k + 1] = g.y;
   }
   if (grew) {
-    // round the older codes again; a lane takes its own four channels of
-    // every row, so it also has their range
+    // round the older codes again, 32 rows in flight; a lane takes its own
+    // four channels of every row, so it also has their range
     const float ratio = __fdiv_rn(s_old, s);
-#pragma unroll 4
-    for (int r = 0; r < lo; ++r) {
-      uint8_t* row = codes + r * kHeadDim;
-      uint32_t w;
-      if (kHalf) {
-        w = *reinterpret_cast<const uint16_t*>(row + c0) |
-            (uint32_t(*reinterpret_cast<const uint16_t*>(row + c1)) << 16);
-      } else {
-        w = *reinterpret_cast<const uint32_t*>(row + c0);
+    constexpr int kRows = 32;
+    for (int r0 = 0; r0 < lo; r0 += kRows) {
+      uint32_t w[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        w[i] = 0;
+        if (r0 + i >= lo) continue;
+        const uint8_t* row = codes + (r0 + i) * kHeadDim;
+        if (kHalf) {
+          w[i] = *reinterpret_cast<const uint16_t*>(row + c0) |
+                 (uint32_t(*reinterpret_cast<const uint16_t*>(row + c1)) << 16);
+        } else {
+          w[i] = *reinterpret_cast<const uint32_t*>(row + c0);
+        }
       }
-      w = recode4<kInt8>(w, ratio);
-      if (kHalf) {
-        *reinterpret_cast<uint16_t*>(row + c0) = uint16_t(w);
-        *reinterpret_cast<uint16_t*>(row + c1) = uint16_t(w >> 16);
-      } else {
-        *reinterpret_cast<uint32_t*>(row + c0) = w;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (r0 + i >= lo) break;
+        uint8_t* row = codes + (r0 + i) * kHeadDim;
+        const uint32_t u = recode4<kInt8>(w[i], ratio);
+        if (kHalf) {
+          *reinterpret_cast<uint16_t*>(row + c0) = uint16_t(u);
+          *reinterpret_cast<uint16_t*>(row + c1) = uint16_t(u >> 16);
+        } else {
+          *reinterpret_cast<uint32_t*>(row + c0) = u;
+        }
+        const float2 f = dec2<kInt8>(u & 0xffffu), g = dec2<kInt8>(u >> 16);
+        cl[0] = fminf(cl[0], f.x); ch[0] = fmaxf(ch[0], f.x);
+        cl[1] = fminf(cl[1], f.y); ch[1] = fmaxf(ch[1], f.y);
+        cl[2] = fminf(cl[2], g.x); ch[2] = fmaxf(ch[2], g.x);
+        cl[3] = fminf(cl[3], g.y); ch[3] = fmaxf(ch[3], g.y);
       }
-      const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
-      cl[0] = fminf(cl[0], f.x); ch[0] = fmaxf(ch[0], f.x);
-      cl[1] = fminf(cl[1], f.y); ch[1] = fmaxf(ch[1], f.y);
-      cl[2] = fminf(cl[2], g.x); ch[2] = fmaxf(ch[2], g.x);
-      cl[3] = fminf(cl[3], g.y); ch[3] = fmaxf(ch[3], g.y);
     }
   }
   if (!key) return;
@@ -353,8 +355,9 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
   for (int64_t i = blockIdx.x; i < grid.items; i += gridDim.x) {
     const WriteItem it = write_item(a, grid, i);
     if (!it.any) continue;
-    // angles of the thread's tokens, pairs 4c .. 4c + 3
-    float4 cs[kWrPasses][2];
+    const bool full = it.lo == 0 && it.hi == kKv8Block;
+    // angles of the thread's tokens, pairs (4c, 4c + 1), (4c + 2, 4c + 3)
+    float2 cc[kWrPasses][2], ss[kWrPasses][2];
     if (it.key) {
 #pragma unroll
       for (int k = 0; k < kWrPasses; ++k) {
@@ -365,8 +368,12 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                          a.max_pos - 1));
         const float4* tab = reinterpret_cast<const float4*>(
             a.table + int64_t(p) * kHeadDim) + 2 * c;
-        cs[k][0] = __ldg(tab);
-        cs[k][1] = __ldg(tab + 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 f = __ldg(tab + j);
+          cc[k][j] = make_float2(f.x, f.z);
+          ss[k][j] = make_float2(f.y, f.w);
+        }
       }
     }
     for (int h = it.h0; h < it.h1; ++h, ++n) {
@@ -377,52 +384,65 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool ok = mbar_wait(bar(n % kWrStages), (n / kWrStages) & 1,
                                 nullptr, status, kWrWaitNs);
       const uint8_t* tile = smem + (n % kWrStages) * kWrTile;
-      float x[kWrPasses][8];
+      // x, y: first and second members of pairs 4c .. 4c + 3
+      float2 x[kWrPasses][2], y[kWrPasses][2];
 #pragma unroll
       for (int k = 0; k < kWrPasses; ++k) {
         const uint8_t* row = tile + (row0 + k * kWrStep) * (kHeadDim * 2);
-        uint32_t w[4];
         if (kHalf) {
           const uint2 u = *reinterpret_cast<const uint2*>(row + c * 8);
           const uint2 v = *reinterpret_cast<const uint2*>(row + 128 + c * 8);
-          w[0] = u.x; w[1] = u.y; w[2] = v.x; w[3] = v.y;
+          x[k][0] = make_float2(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x));
+          x[k][1] = make_float2(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+          y[k][0] = make_float2(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x));
+          y[k][1] = make_float2(bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
         } else {
           const uint4 u = *reinterpret_cast<const uint4*>(row + c * 16);
-          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+          x[k][0] = make_float2(bf16lo_to_f32(u.x), bf16lo_to_f32(u.y));
+          y[k][0] = make_float2(bf16hi_to_f32(u.x), bf16hi_to_f32(u.y));
+          x[k][1] = make_float2(bf16lo_to_f32(u.z), bf16lo_to_f32(u.w));
+          y[k][1] = make_float2(bf16hi_to_f32(u.z), bf16hi_to_f32(u.w));
         }
+        if (it.key) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[k][2 * j] = bf16lo_to_f32(w[j]);
-          x[k][2 * j + 1] = bf16hi_to_f32(w[j]);
+          for (int j = 0; j < 2; ++j) {
+            const float2 p = x[k][j], q = y[k][j];
+            x[k][j] = sub2(mul2(p, cc[k][j]), mul2(q, ss[k][j]));
+            y[k][j] = add2(mul2(p, ss[k][j]), mul2(q, cc[k][j]));
+          }
         }
       }
-      float mn[8], mx[8], amax = 0.f;
+      float amax = 0.f;
+      // value j of pass k: x of pairs 4c + j for j < 4, then their y
+      auto val = [&](int k, int j) {
+        const float2 v = j < 4 ? x[k][j / 2] : y[k][(j - 4) / 2];
+        return (j & 1) ? v.y : v.x;
+      };
+      static_assert(kWrPasses == 4, "the maxima below take four values");
       if (it.key) {
+        float mn[8], mx[8];
+        bool some = false;
+        if (full) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mn[j] = INFINITY;
-          mx[j] = -INFINITY;
-        }
-#pragma unroll
-        for (int k = 0; k < kWrPasses; ++k) {
-          const float4 q0 = cs[k][0], q1 = cs[k][1];
-          if (kHalf) {
-            rotate(x[k][0], x[k][4], q0.x, q0.y);
-            rotate(x[k][1], x[k][5], q0.z, q0.w);
-            rotate(x[k][2], x[k][6], q1.x, q1.y);
-            rotate(x[k][3], x[k][7], q1.z, q1.w);
-          } else {
-            rotate(x[k][0], x[k][1], q0.x, q0.y);
-            rotate(x[k][2], x[k][3], q0.z, q0.w);
-            rotate(x[k][4], x[k][5], q1.x, q1.y);
-            rotate(x[k][6], x[k][7], q1.z, q1.w);
+          for (int j = 0; j < 8; ++j) {
+            mn[j] = min_nan(min3_nan(val(0, j), val(1, j), val(2, j)),
+                            val(3, j));
+            mx[j] = max_nan(max3_nan(val(0, j), val(1, j), val(2, j)),
+                            val(3, j));
           }
-          const int r = row0 + k * kWrStep;
-          if (r >= it.lo && r < it.hi) {
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              mn[j] = min_nan(mn[j], x[k][j]);
-              mx[j] = max_nan(mx[j], x[k][j]);
+          for (int j = 0; j < 8; ++j) {
+            mn[j] = INFINITY;
+            mx[j] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWrPasses; ++k) {
+              const int r = row0 + k * kWrStep;
+              if (r >= it.lo && r < it.hi) {
+                some = true;
+                mn[j] = min_nan(mn[j], val(k, j));
+                mx[j] = max_nan(mx[j], val(k, j));
+              }
             }
           }
         }
@@ -433,37 +453,42 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         float* chan = reinterpret_cast<float*>(smem + kWrChan) +
                       ((n & 1) * 2 * kWrWarps + warp) * kHeadDim;
-        if (lane < kWrLanes) {
-          // interleaved: channels 8c ..; half: 4c .. and 64 + 4c ..
-          float* lo4 = chan + (kHalf ? 4 * c : 8 * c);
-          float* hi4 = kHalf ? lo4 + 64 : lo4 + 4;
-          *reinterpret_cast<float4*>(lo4) =
-              make_float4(mn[0], mn[1], mn[2], mn[3]);
-          *reinterpret_cast<float4*>(hi4) =
-              make_float4(mn[4], mn[5], mn[6], mn[7]);
-          *reinterpret_cast<float4*>(lo4 + kWrWarps * kHeadDim) =
-              make_float4(mx[0], mx[1], mx[2], mx[3]);
-          *reinterpret_cast<float4*>(hi4 + kWrWarps * kHeadDim) =
-              make_float4(mx[4], mx[5], mx[6], mx[7]);
-        }
-        // a warp none of whose tokens is new has mn > mx
+        // lanes 0-15 keep the smallest values, the others the largest
+        const bool low = lane < kWrLanes;
+        float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!(mn[j] > mx[j]))
-            amax = max_nan(amax, max_nan(fabsf(mn[j]), fabsf(mx[j])));
+        for (int j = 0; j < 8; ++j) m[j] = low ? mn[j] : mx[j];
+        if (!low) chan += kWrWarps * kHeadDim;
+        if (kHalf) {    // channels 4c .. and 64 + 4c ..
+          *reinterpret_cast<float4*>(chan + 4 * c) =
+              make_float4(m[0], m[1], m[2], m[3]);
+          *reinterpret_cast<float4*>(chan + 64 + 4 * c) =
+              make_float4(m[4], m[5], m[6], m[7]);
+        } else {        // channels 8c .., pairs side by side
+          *reinterpret_cast<float4*>(chan + 8 * c) =
+              make_float4(m[0], m[4], m[1], m[5]);
+          *reinterpret_cast<float4*>(chan + 8 * c + 4) =
+              make_float4(m[2], m[6], m[3], m[7]);
+        }
+        // a warp none of whose tokens is new has nothing to add
+        if (full || __any_sync(0xffffffffu, some)) {
+          amax = max3_abs_nan(max3_abs_nan(m[0], m[1], m[2]),
+                              max3_abs_nan(m[3], m[4], m[5]),
+                              max_nan(fabsf(m[6]), fabsf(m[7])));
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < kWrPasses; ++k) {
           const int r = row0 + k * kWrStep;
-          if (r >= it.lo && r < it.hi) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[k][j]));
+          if (full || (r >= it.lo && r < it.hi)) {
+            amax = max3_abs_nan(amax, x[k][0].x, x[k][0].y);
+            amax = max3_abs_nan(amax, x[k][1].x, x[k][1].y);
+            amax = max3_abs_nan(amax, y[k][0].x, y[k][0].y);
+            amax = max3_abs_nan(amax, y[k][1].x, y[k][1].y);
           }
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      amax = warp_max_abs(amax);
       float* red = reinterpret_cast<float*>(smem + kWrMax) +
                    (n & 1) * kWrWarps;
       if (lane == 0) red[warp] = amax;
@@ -487,14 +512,22 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool grew = it.lo > 0 && s > s_old;
       uint8_t* codes = static_cast<uint8_t*>(it.key ? a.codes[0] : a.codes[1]) +
                        (bh * a.L + it.base) * kHeadDim;
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
       for (int k = 0; k < kWrPasses; ++k) {
         const int r = row0 + k * kWrStep;
-        if (r < it.lo || r >= it.hi) continue;
-        const uint32_t w0 = code2<kInt8>(x[k][0], x[k][1], inv) |
-                            (code2<kInt8>(x[k][2], x[k][3], inv) << 16);
-        const uint32_t w1 = code2<kInt8>(x[k][4], x[k][5], inv) |
-                            (code2<kInt8>(x[k][6], x[k][7], inv) << 16);
+        if (!full && (r < it.lo || r >= it.hi)) continue;
+        const float2 x0 = mul2(x[k][0], inv2), x1 = mul2(x[k][1], inv2);
+        const float2 y0 = mul2(y[k][0], inv2), y1 = mul2(y[k][1], inv2);
+        uint32_t w0, w1;
+        if (kHalf) {
+          w0 = enc4<kInt8>(x0.x, x0.y, x1.x, x1.y);
+          w1 = enc4<kInt8>(y0.x, y0.y, y1.x, y1.y);
+        } else {
+          w0 = enc4<kInt8>(x0.x, y0.x, x0.y, y0.y);
+          w1 = enc4<kInt8>(x1.x, y1.x, x1.y, y1.y);
+        }
+        if (!(inv > 0.f)) w0 = w1 = 0u;     // whatever the values are
         uint8_t* row = codes + r * kHeadDim;
         if (kHalf) {
           *reinterpret_cast<uint32_t*>(row + c * 4) = w0;
