@@ -3,6 +3,8 @@
 // (tensor memory alloc, MMA, commit, ld/st) and bounded waits.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -18,6 +20,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Device status word values (written with atomicMax so the worst wins).
 constexpr int kStatusTimeout = LWM_ERR_TIMEOUT;
+
+// Devices whose constants (SM count, symbol addresses, opted-in shared
+// memory) the host side looks up once.
+constexpr int kKnownDevices = 64;
 
 // Host-side count of kernel launches made by the library (see
 // lwm_blockattn_kernel_launches); launch helpers call note_launch().
@@ -366,6 +372,21 @@ __device__ __forceinline__ void pdl_wait() {
 }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Lets `Kernel` use `bytes` of dynamic shared memory on the current device;
+// asks the runtime once per kernel and device.
+template <auto Kernel>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<int> allowed[kKnownDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kKnownDevices && allowed[dev].load() >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(
+      Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kKnownDevices) allowed[dev].store(bytes);
+  return e;
 }
 
 template <typename... KArgs, typename... Args>

@@ -967,11 +967,15 @@ bool make_bnhd_f32_map(CUtensorMap* m, const void* base, int B, int N,
 }
 
 int sm_count() {
+  // asked once per device: a call may need it several times
+  static std::atomic<int> known[kKnownDevices];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < kKnownDevices && (n = known[dev].load()) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
       cudaSuccess)
     return 148;
+  if (dev < kKnownDevices) known[dev].store(n);
   return n;
 }
 

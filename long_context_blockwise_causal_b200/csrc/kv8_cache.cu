@@ -697,9 +697,7 @@ cudaError_t launch_many(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
       1, std::min<int64_t>({16, tiles / (4 * sms), a.H})));
   g.groups = (a.H + g.heads - 1) / g.heads;
   g.items = 2 * int64_t(a.B) * g.per_row * g.groups;
-  cudaError_t e = cudaFuncSetAttribute(
-      kv8_write_kernel<kInt8, kHalf>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, kWrSmem);
+  const cudaError_t e = allow_smem<kv8_write_kernel<kInt8, kHalf>>(kWrSmem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = std::min<int64_t>(g.items, sms);
   return launch_dependent(kv8_write_kernel<kInt8, kHalf>,

@@ -135,10 +135,9 @@ enum : int {
   kSlot1 = 8,     // partial result goes to the CTA's second record
   kEnd = 16,      // no tile: the CTA's work is done
 };
-struct __align__(16) Tile {
+struct __align__(8) Tile {
   int b, h, blk, flags;
   int lo, hi;     // visible slots of the block (lo >= hi: nothing to read)
-  float ks, vs;
 };
 
 template <bool kInt8, int GP>
@@ -409,10 +408,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int s = i % C::kStages;
         const bool live = cur.lo < cur.hi;
         const int64_t bh = int64_t(cur.b) * a.H + cur.h;
-        if (live) {
-          cur.ks = __ldg(a.k_scale + bh * nblk + cur.blk);
-          cur.vs = __ldg(a.v_scale + bh * nblk + cur.blk);
-        }
         more = w.next(nxt);
         if (!more || (nxt.flags & kFirst)) cur.flags |= kLast;
         if (i >= C::kStages) ok = wait(C::bEmpty + s, i / C::kStages - 1);
@@ -578,7 +573,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     bool ok = wait(C::bTok, 0);
     bool go = softmax_all(ok);
     Tile cur = ring[0];
+    // scales of a tile, fetched while the tile before it is worked on
+    float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+    auto fetch = [&](const Tile& x) {
+      if (x.lo >= x.hi) return;
+      const int64_t i = (int64_t(x.b) * a.H + x.h) * nblk + x.blk;
+      ks_next = __ldg(a.k_scale + i);
+      vs_next = __ldg(a.v_scale + i);
+    };
     if (go && !(cur.flags & kEnd)) {
+      fetch(cur);
       make_q(cur.b, cur.h, 0);
       seg = 0;
     }
@@ -607,6 +611,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool live = cur.lo < cur.hi;
       ok = wait(C::bTok + (i + 1) % kDecRing, (i + 1) / kDecRing) && ok;
       const Tile nxt = ring[(i + 1) % kDecRing];
+      ks = ks_next;
+      vs = vs_next;
+      if (ok && !(nxt.flags & kEnd)) fetch(nxt);
       if (cur.flags & kFirst) {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
@@ -638,7 +645,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int n = C::kQTerms - 2; n >= 0; --n)
               x = fmaf(x, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
-            s[g] = seen ? x * (cur.ks * qscale[(seg & 1) * GP + g])
+            s[g] = seen ? x * (ks * qscale[(seg & 1) * GP + g])
                         : -INFINITY;
           }
         }
@@ -663,7 +670,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           m[g] = mn;
           l[g] = fmaf(p[g], be[g], l[g] * al[g]);
           p[g] *= C::kPScale;
-          be[g] *= cur.vs * (1.f / C::kPScale);
+          be[g] *= vs * (1.f / C::kPScale);
         }
         uint8_t* dst = smem + C::kP + (i & 1) * C::kPBytes;
 #pragma unroll
@@ -878,9 +885,7 @@ cudaError_t launch_tiles(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
   if (!make_codes_map(&mk, k, int64_t(a.B) * a.H, L) ||
       !make_codes_map(&mv, v, int64_t(a.B) * a.H, L))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(
-      kv8_decode_kernel<kInt8, GP>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmem);
+  const cudaError_t e = allow_smem<kv8_decode_kernel<kInt8, GP>>(D::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv8_decode_kernel<kInt8, GP>, dim3(C),
                           dim3(kDecThreads), D::kSmem, st, mk, mv, a);

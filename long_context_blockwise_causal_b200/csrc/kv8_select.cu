@@ -293,9 +293,7 @@ cudaError_t launch_kv8_select(const Kv8SelectArgs& a, cudaStream_t st) {
   while (C < 8 && nblk > 128 * C) C *= 2;
   const int64_t grid = int64_t(a.B) * a.H * C;
   const size_t smem = size_t((nblk + C - 1) / C) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(
-      kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      int(smem));
+  cudaError_t e = allow_smem<kv8_select_kernel>(int(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));

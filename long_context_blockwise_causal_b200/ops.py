@@ -647,38 +647,85 @@ def kv8_cache(B, L, H, dtype=torch.float8_e4m3fn, D=HEAD_DIM,
                     z((B, H, n, 2, D), torch.int8))
 
 
-def _check_kv8(where, cache, *others):
-    """Shapes, types and placement of a cache; returns (B, H, L, D, type)."""
-    k, v, ks, vs, kb = cache
-    _expect_dims(where, "cache.k", k, 4)
+def _kv8_sizes(where, cache):
+    """(B, H, L, D, type code) of a cache whose k and v have them."""
+    k = cache.k
     code = _KV8_TYPES.get(k.dtype)
     if code is None:
         raise LwmError(ERR_INVALID_ARG, f"{where}: cache.k is {k.dtype}")
+    _expect_dims(where, "cache.k", k, 4)
     B, H, L, D = k.shape
-    n = -(-L // BLOCK)
-    _expect(where, "cache.v", v, k.shape, k.dtype)
-    _expect(where, "cache.k_scale", ks, (B, H, n), torch.float32)
-    _expect(where, "cache.v_scale", vs, (B, H, n), torch.float32)
-    _expect(where, "cache.k_bounds", kb, (B, H, n, 2, D), torch.int8)
-    _same_device(where, k, v, ks, vs, kb, *others)
     return B, H, L, D, code
 
 
-def _check_kv8_query(where, q, B, H, D, kv_start, kv_len, q_pos, table):
-    """q [B,Hq,D] with Hq a multiple of H; returns Hq."""
+def _kv8_group(where, q, B, H, D):
+    """Query heads of q [B,Hq,D], a multiple of the cache's H heads."""
     _expect_dims(where, "q", q, 3)
-    _expect_dims(where, "table", table, 3)
     Hq = q.shape[1]
-    _expect(where, "q", q, (B, Hq, D), torch.bfloat16)
     if H and Hq % H:
         raise LwmError(ERR_INVALID_ARG,
                        f"{where}: {Hq} query heads over {H} cache heads")
-    for name, t in (("kv_start", kv_start), ("kv_len", kv_len),
-                    ("q_pos", q_pos)):
-        _expect(where, name, t, (B,), torch.int32)
-    _expect(where, "table", table, (table.shape[0], D // 2, 2),
-            torch.float32)
     return Hq
+
+
+def _kv8_ready(where, cache, B, H, L, D, table, named):
+    """Shapes, types and placement of every tensor of a call, before any
+    pointer reaches the library: the cache's, table's and the (name, tensor
+    or None, shape, dtype) of `named`. One pass, as these calls are short."""
+    k, v, ks, vs, kb = cache
+    n = (L + BLOCK - 1) // BLOCK
+    scales = (B, H, n)
+    bad = (v.shape != k.shape or v.dtype is not k.dtype
+           or ks.shape != scales or ks.dtype is not torch.float32
+           or vs.shape != scales or vs.dtype is not torch.float32
+           or kb.shape != (B, H, n, 2, D) or kb.dtype is not torch.int8)
+    if table is not None:
+        tshape = table.shape
+        bad = bad or (len(tshape) != 3 or tshape[1:] != (D // 2, 2)
+                      or table.dtype is not torch.float32)
+    dev = k.get_device()
+    placed = [k, v, ks, vs, kb]
+    if table is not None:
+        placed.append(table)
+    for _, t, shape, dtype in named:
+        if t is not None:
+            bad = bad or t.shape != shape or t.dtype is not dtype
+            placed.append(t)
+    if bad:
+        _expect(where, "cache.v", v, k.shape, k.dtype)
+        _expect(where, "cache.k_scale", ks, scales, torch.float32)
+        _expect(where, "cache.v_scale", vs, scales, torch.float32)
+        _expect(where, "cache.k_bounds", kb, (B, H, n, 2, D), torch.int8)
+        if table is not None:
+            _expect_dims(where, "table", table, 3)
+            _expect(where, "table", table, (table.shape[0], D // 2, 2),
+                    torch.float32)
+        for name, t, shape, dtype in named:
+            _expect(where, name, t, shape, dtype)
+    for t in placed:
+        if t.get_device() != dev:
+            _same_device(where, *placed)
+        if dev < 0 or not t.is_contiguous():
+            _need_cuda(*placed)
+    return dev
+
+
+def _kv8_call(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current; the stream is by
+    default that device's current one."""
+    if stream is None:
+        # the current stream's handle, without building a Stream object
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
+    call = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == dev:
+        st = call(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, handle)
+    if st != OK:
+        raise LwmError(st, fn)
 
 
 def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
@@ -687,26 +734,22 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
     start[b] + t (in place; see the header for the block scales). ``n_new``
     [B]: new tokens of a padded row. Returns the cache."""
     w = "kv8_write"
-    B, H, L, D, code = _check_kv8(w, cache, k, v, positions, start, table,
-                                  n_new)
+    B, H, L, D, code = _kv8_sizes(w, cache)
     _expect_dims(w, "k", k, 4)
-    _expect_dims(w, "table", table, 3)
     T = k.shape[1]
-    _expect(w, "k", k, (B, T, H, D), torch.bfloat16)
-    _expect(w, "v", v, (B, T, H, D), torch.bfloat16)
-    _expect(w, "positions", positions, (B, T), torch.int32)
-    _expect(w, "start", start, (B,), torch.int32)
-    _expect(w, "n_new", n_new, (B,), torch.int32)
-    _expect(w, "table", table, (table.shape[0], D // 2, 2), torch.float32)
-    _need_cuda(*cache, k, v, positions, start, table, n_new)
-    with torch.cuda.device(k.device):
-        st = lib().lwm_kv8_write(
-            _ptr(k), _ptr(v), _ptr(positions), _ptr(start), _ptr(n_new),
-            _ptr(table), table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
-            _layout_code(rope_layout), _ptr(cache.k), _ptr(cache.v),
-            _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(cache.k_bounds),
-            _stream(stream))
-    _check(st, "lwm_kv8_write")
+    new = (B, T, H, D)
+    dev = _kv8_ready(w, cache, B, H, L, D, table, (
+        ("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
+        ("positions", positions, (B, T), torch.int32),
+        ("start", start, (B,), torch.int32),
+        ("n_new", n_new, (B,), torch.int32)))
+    _kv8_call("lwm_kv8_write", dev, stream, k.data_ptr(), v.data_ptr(),
+              positions.data_ptr(), start.data_ptr(),
+              None if n_new is None else n_new.data_ptr(), table.data_ptr(),
+              table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
+              _layout_code(rope_layout), cache.k.data_ptr(),
+              cache.v.data_ptr(), cache.k_scale.data_ptr(),
+              cache.v_scale.data_ptr(), cache.k_bounds.data_ptr())
     return cache
 
 
@@ -715,25 +758,25 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     [B,T,H,D], zeros outside [0, min(kv_len[b], L)); the layout fwd_block
     takes rotated keys and values in."""
     w = "kv8_read"
-    B, H, L, D, code = _check_kv8(w, cache, start, kv_len, k_rot, v)
-    _expect(w, "start", start, (B,), torch.int32)
-    _expect(w, "kv_len", kv_len, (B,), torch.int32)
+    B, H, L, D, code = _kv8_sizes(w, cache)
     T = int(T)
     if T < 0:
         raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
-    _expect(w, "k_rot", k_rot, (B, T, H, D), torch.bfloat16)
-    _expect(w, "v", v, (B, T, H, D), torch.bfloat16)
-    _need_cuda(*cache, start, kv_len, k_rot, v)
-    new = lambda: torch.empty((B, T, H, D), dtype=torch.bfloat16,
-                              device=cache.k.device)
-    k_rot = new() if k_rot is None else k_rot
-    v = new() if v is None else v
-    with torch.cuda.device(cache.k.device):
-        st = lib().lwm_kv8_read(
-            _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
-            _ptr(cache.v_scale), _ptr(start), _ptr(kv_len), B, T, L, H, D,
-            DTYPE_BF16, code, _ptr(k_rot), _ptr(v), _stream(stream))
-    _check(st, "lwm_kv8_read")
+    shape = (B, T, H, D)
+    dev = _kv8_ready(w, cache, B, H, L, D, None, (
+        ("start", start, (B,), torch.int32),
+        ("kv_len", kv_len, (B,), torch.int32),
+        ("k_rot", k_rot, shape, torch.bfloat16),
+        ("v", v, shape, torch.bfloat16)))
+    if k_rot is None:
+        k_rot = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
+    if v is None:
+        v = torch.empty_like(k_rot)
+    _kv8_call("lwm_kv8_read", dev, stream, cache.k.data_ptr(),
+              cache.v.data_ptr(), cache.k_scale.data_ptr(),
+              cache.v_scale.data_ptr(), start.data_ptr(),
+              None if kv_len is None else kv_len.data_ptr(), B, T, L, H, D,
+              DTYPE_BF16, code, k_rot.data_ptr(), v.data_ptr())
     return k_rot, v
 
 
@@ -745,27 +788,28 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     fp32) [B,H,n_select], ascending, (-1, -inf) behind a short list. The
     first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
     w = "kv8_select"
-    B, H, L, D, _ = _check_kv8(w, cache, q, kv_start, kv_len, q_pos, table,
-                               blocks, scores)
-    Hq = _check_kv8_query(w, q, B, H, D, kv_start, kv_len, q_pos, table)
+    B, H, L, D, _ = _kv8_sizes(w, cache)
+    Hq = _kv8_group(w, q, B, H, D)
     K = int(n_select)
     if K < 1:
         raise LwmError(ERR_INVALID_ARG, f"{w}: n_select is {K}")
-    _expect(w, "blocks", blocks, (B, H, K), torch.int32)
-    _expect(w, "scores", scores, (B, H, K), torch.float32)
-    _need_cuda(*cache, q, kv_start, kv_len, q_pos, table, blocks, scores)
+    dev = _kv8_ready(w, cache, B, H, L, D, table, (
+        ("q", q, (B, Hq, D), torch.bfloat16),
+        ("kv_start", kv_start, (B,), torch.int32),
+        ("kv_len", kv_len, (B,), torch.int32),
+        ("q_pos", q_pos, (B,), torch.int32),
+        ("blocks", blocks, (B, H, K), torch.int32),
+        ("scores", scores, (B, H, K), torch.float32)))
     if blocks is None:
         blocks = torch.empty((B, H, K), dtype=torch.int32, device=q.device)
     if scores is None:
-        scores = torch.empty((B, H, K), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
-        st = lib().lwm_kv8_select(
-            _ptr(q), _ptr(cache.k_bounds), _ptr(cache.k_scale),
-            _ptr(kv_start), _ptr(kv_len), _ptr(q_pos), _ptr(table),
-            table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
-            _layout_code(rope_layout), K, int(n_sink), int(n_recent),
-            _ptr(blocks), _ptr(scores), _stream(stream))
-    _check(st, "lwm_kv8_select")
+        scores = torch.empty_like(blocks, dtype=torch.float32)
+    _kv8_call("lwm_kv8_select", dev, stream, q.data_ptr(),
+              cache.k_bounds.data_ptr(), cache.k_scale.data_ptr(),
+              kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
+              table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
+              _layout_code(rope_layout), K, int(n_sink), int(n_recent),
+              blocks.data_ptr(), scores.data_ptr())
     return blocks, scores
 
 
@@ -782,33 +826,37 @@ def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
     [B,H,n] (a list of kv8_select, strictly ascending). Query head i reads
     cache head i // (Hq // H). Returns (out [B,Hq,D], lse [B,Hq])."""
     w = "kv8_decode"
-    B, H, L, D, code = _check_kv8(w, cache, q, kv_start, kv_len, q_pos,
-                                  table, blocks, out, lse, workspace)
-    Hq = _check_kv8_query(w, q, B, H, D, kv_start, kv_len, q_pos, table)
+    B, H, L, D, code = _kv8_sizes(w, cache)
+    Hq = _kv8_group(w, q, B, H, D)
     K = -1
     if blocks is not None:
         _expect_dims(w, "blocks", blocks, 3)
         K = blocks.shape[2]
-        _expect(w, "blocks", blocks, (B, H, K), torch.int32)
-    _expect(w, "out", out, q.shape, q.dtype)
-    _expect(w, "lse", lse, (B, Hq), torch.float32)
-    _need_cuda(*cache, q, kv_start, kv_len, q_pos, table, blocks, out, lse,
-               workspace)
-    out = torch.empty_like(q) if out is None else out
+    dev = _kv8_ready(w, cache, B, H, L, D, table, (
+        ("q", q, (B, Hq, D), torch.bfloat16),
+        ("kv_start", kv_start, (B,), torch.int32),
+        ("kv_len", kv_len, (B,), torch.int32),
+        ("q_pos", q_pos, (B,), torch.int32),
+        ("blocks", blocks, (B, H, K), torch.int32),
+        ("out", out, (B, Hq, D), torch.bfloat16),
+        ("lse", lse, (B, Hq), torch.float32),
+        ("workspace", workspace, getattr(workspace, "shape", None),
+         getattr(workspace, "dtype", None))))
+    if out is None:
+        out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    ws = _workspace(int(lib().lwm_kv8_decode_workspace_size(B, L, Hq, H, D,
-                                                            K)),
-                    q.device, workspace)
-    with torch.cuda.device(q.device):
-        st = lib().lwm_kv8_decode(
-            _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
-            _ptr(cache.v_scale), _ptr(kv_start), _ptr(kv_len), _ptr(q_pos),
-            _ptr(blocks), K, _ptr(table), table.shape[0], B, L, Hq, H, D,
-            DTYPE_BF16, code, _layout_code(rope_layout), _ptr(out),
-            _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
-            _stream(stream))
-    _check(st, "lwm_kv8_decode")
+    ws = _workspace(
+        lib().lwm_kv8_decode_workspace_size(B, L, Hq, H, D, K), q.device,
+        workspace)
+    _kv8_call("lwm_kv8_decode", dev, stream, q.data_ptr(),
+              cache.k.data_ptr(), cache.v.data_ptr(),
+              cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+              kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
+              None if blocks is None else blocks.data_ptr(), K,
+              table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
+              code, _layout_code(rope_layout), out.data_ptr(),
+              lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return out, lse
 
 
