@@ -16,9 +16,12 @@
 namespace lwm {
 namespace {
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 256;
+constexpr int kSelPasses = 3;                // digits of 11, 11 and 10 bits
+constexpr int kSelBins = 2048;
+constexpr int kSelFlight = 4;                // pairs of blocks in flight
+constexpr int kSelMost = 8;                  // CTAs per cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -30,14 +33,17 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same shared-memory word in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_load(const uint32_t* p,
-                                              uint32_t rank) {
-  uint32_t at, v;
+// Four words of CTA `rank`'s shared memory, from the place where this CTA
+// has them.
+__device__ __forceinline__ uint4 peer_load4(const uint32_t* p, uint32_t rank) {
+  uint32_t at;
+  uint4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(at)
                : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at)
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
                : "memory");
   return v;
 }
@@ -50,9 +56,9 @@ __device__ __forceinline__ uint32_t rank_key(float s, bool forced) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Sum over the block's threads of (x, y), for every thread.
-__device__ __forceinline__ uint2 block_prefix(uint32_t x, uint2* buf,
-                                              uint32_t* total) {
+// Sum of x over the threads before this one; *total: over all of them.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* buf,
+                                                 uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t inc = x;
 #pragma unroll
@@ -60,39 +66,67 @@ __device__ __forceinline__ uint2 block_prefix(uint32_t x, uint2* buf,
     const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  if (lane == 31) buf[warp].x = inc;
+  if (lane == 31) buf[warp] = inc;
   __syncthreads();
   uint32_t before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kSelWarps; ++w) {
-    const uint32_t y = buf[w].x;
-    if (w < warp) before += y;
+    const uint32_t y = buf[w];
+    before += w < warp ? y : 0u;
     all += y;
   }
   __syncthreads();
   *total = all;
-  return make_uint2(before + inc - x, before + inc);
+  return before + inc - x;
+}
+
+// Adds up GP values over the 16 lanes that share a block, halving the number
+// of values a lane holds while it can: lane l ends with the total of value
+// l mod GP (in v[0]).
+template <int GP>
+__device__ __forceinline__ int sum16(int (&v)[GP]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = GP / 2; o > 0; o >>= 1) {
+    // of 2 o values, those whose index has bit o go to the lanes that have it
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const int keep = up ? v[i + o] : v[i];
+      const int give = up ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (int o = GP; o < 16; o <<= 1)
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
 
 // A cluster of C CTAs per (row, cache head); CTA r scores the r-th share of
 // the visible blocks into its shared memory, and the cluster finds the K-th
-// best key by four rounds of 8-bit counting over all its shares.
-__global__ void __launch_bounds__(kSelThreads)
-kv8_select_kernel(const Kv8SelectArgs a, int C) {
-  pdl_wait();
-  pdl_trigger();
+// best key by three rounds of digit counting over all its shares. Bound by
+// reading the bounds (256 bytes per block): 16 lanes share a block, a warp
+// keeps 4 pairs of blocks in flight. GP: G rounded up to a power of two.
+template <int GP>
+__global__ void __launch_bounds__(kSelThreads, 2)
+kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   extern __shared__ float score[];                    // [share]
-  __shared__ __align__(16) int8_t qc[kKv8MaxGroup][2 * kHeadDim];
-  __shared__ double qs[kKv8MaxGroup];
-  __shared__ double qmax[kSelWarps];
-  __shared__ uint32_t hist[4][kSelBins];
-  __shared__ uint32_t counts[2];                      // above, equal
-  __shared__ uint2 scan[kSelWarps];
+  __shared__ __align__(16) int8_t qc[GP][2 * kHeadDim];
+  __shared__ double qs[GP];
+  __shared__ __align__(16) uint32_t hist[kSelPasses][kSelBins];
+  __shared__ __align__(16) uint32_t counts[4];        // above, equal
+  __shared__ uint32_t scan[kSelWarps];
   __shared__ uint32_t pick[2];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = int(cluster_rank());
   const int64_t bh = blockIdx.x / C;
-  const int b = int(bh / a.H), h = int(bh % a.H);
+  const int b = int(bh / a.H), h = int(bh - int64_t(b) * a.H);
+  for (int i = t; i < kSelPasses * kSelBins; i += kSelThreads)
+    hist[0][i] = 0;
+  if (t < 4) counts[t] = 0;
+  pdl_wait();
+  pdl_trigger();
 
   const int len = max(0, min(__ldg(a.kv_len + b), a.L));
   const int start = max(0, min(__ldg(a.kv_start + b), len));
@@ -103,84 +137,116 @@ kv8_select_kernel(const Kv8SelectArgs a, int C) {
   const int i0 = min(r * share, nv), n = min(share, nv - i0);
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
 
-  for (int i = t; i < 4 * kSelBins; i += kSelThreads)
-    hist[i / kSelBins][i % kSelBins] = 0;
-
-  // query codes: qc[g] = (min(qi, 0), max(qi, 0)), as the bounds lie
+  // query codes: qc[g] = (min(qi, 0), max(qi, 0)), as the bounds lie; a warp
+  // per head, two pairs of the rotation per lane
   const int p = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
-  for (int g = 0; g < a.G; ++g) {
-    double x = 0.0;
-    const int d = t & (kHeadDim - 1);
-    {
-      const __nv_bfloat16* q =
-          static_cast<const __nv_bfloat16*>(a.q) +
-          (int64_t(b) * a.H * a.G + h * a.G + g) * kHeadDim;
-      const int k = a.half ? (d & 63) : (d >> 1);
-      const bool low = a.half ? d < 64 : (d & 1) == 0;
-      const int i_a = a.half ? k : 2 * k, i_b = a.half ? k + 64 : 2 * k + 1;
-      const float2 cs = __ldg(reinterpret_cast<const float2*>(a.table) +
-                              int64_t(p) * (kHeadDim / 2) + k);
-      const double qa = double(__bfloat162float(q[i_a]));
-      const double qb = double(__bfloat162float(q[i_b]));
-      x = low ? __dsub_rn(__dmul_rn(qa, double(cs.x)),
-                          __dmul_rn(qb, double(cs.y)))
-              : __dadd_rn(__dmul_rn(qa, double(cs.y)),
-                          __dmul_rn(qb, double(cs.x)));
+  for (int g = warp; g < GP; g += kSelWarps) {
+    const int c0 = a.half ? 2 * lane : 4 * lane;       // channels c0, c0 + 1,
+    const int c1 = a.half ? 64 + 2 * lane : c0 + 2;    // c1, c1 + 1
+    double x[4] = {0.0, 0.0, 0.0, 0.0};
+    if (g < a.G) {
+      const char* q = static_cast<const char*>(a.q) +
+                      (bh * a.G + g) * (kHeadDim * 2);
+      const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(q + 2 * c0));
+      const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(q + 2 * c1));
+      const float4 cs = __ldg(reinterpret_cast<const float4*>(
+                                  a.table + int64_t(p) * kHeadDim) + lane);
+      const double f[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0),
+                           bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
+      auto turn = [](double u, double v, double c, double s, double& ru,
+                     double& rv) {
+        ru = __dsub_rn(__dmul_rn(u, c), __dmul_rn(v, s));
+        rv = __dadd_rn(__dmul_rn(u, s), __dmul_rn(v, c));
+      };
+      if (a.half) {
+        turn(f[0], f[2], cs.x, cs.y, x[0], x[2]);
+        turn(f[1], f[3], cs.z, cs.w, x[1], x[3]);
+      } else {
+        turn(f[0], f[1], cs.x, cs.y, x[0], x[1]);
+        turn(f[2], f[3], cs.z, cs.w, x[2], x[3]);
+      }
     }
-    double m = fabs(x);
-    bool bad = !(m <= 1e300);
+    double m = 0.0;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      bad = bad || !(fabs(x[k]) <= 1e300);
+      m = fmax(m, fabs(x[k]));
+    }
+    bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) qmax[warp] = m;
-    bad = __syncthreads_or(bad);
-    m = 0.0;
+    const double f = m > 0.0 && !bad ? 127.0 / m : 0.0;
+    int qi[4];
 #pragma unroll
-    for (int w = 0; w < kHeadDim / 32; ++w) m = fmax(m, qmax[w]);
-    int qi = 0;
-    if (m > 0.0 && !bad) qi = __double2int_rn(__dmul_rn(x, 127.0 / m));
-    qi = max(-127, min(127, qi));
-    if (t < kHeadDim) {
-      qc[g][d] = int8_t(min(qi, 0));
-      qc[g][kHeadDim + d] = int8_t(max(qi, 0));
+    for (int k = 0; k < 4; ++k) {
+      qi[k] = f > 0.0 ? __double2int_rn(__dmul_rn(x[k], f)) : 0;
+      qi[k] = max(-127, min(127, qi[k]));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const int c = k ? c1 : c0;
+      *reinterpret_cast<char2*>(&qc[g][c]) =
+          make_char2(char(min(qi[k], 0)), char(min(qi[k + 1], 0)));
+      *reinterpret_cast<char2*>(&qc[g][kHeadDim + c]) =
+          make_char2(char(max(qi[k], 0)), char(max(qi[k + 1], 0)));
     }
     // a query with a NaN or an infinity scores every block alike
-    if (t == 0) qs[g] = bad ? 0.0 : __dmul_rn(m, 1.0 / 127.0);
-    __syncthreads();
+    if (lane == 0) qs[g] = bad ? 0.0 : __dmul_rn(m, 1.0 / 127.0);
   }
+  __syncthreads();
 
   // scores: 16 lanes per block, 16 of its 256 bounds each
   {
     const int l16 = lane & 15;
-    const int step = kSelWarps * 2;
     const int8_t* bounds =
-        a.k_bounds + (bh * nblk + j0 + i0) * (2 * kHeadDim);
+        a.k_bounds + (bh * nblk + j0 + i0) * (2 * kHeadDim) + l16 * 16;
     const float* ks = a.k_scale + bh * nblk + j0 + i0;
-    for (int i = warp * 2; i < n; i += step) {
-      const int blk = i + (lane >> 4);
-      const bool on = blk < n;
-      int4 w = make_int4(0, 0, 0, 0);
-      float s = 0.f;
-      if (on) {
-        w = __ldg(reinterpret_cast<const int4*>(
-                bounds + int64_t(blk) * (2 * kHeadDim)) + l16);
-        s = __ldg(ks + blk);
-      }
-      float best = -INFINITY;
-      for (int g = 0; g < a.G; ++g) {
-        const int4 q = *reinterpret_cast<const int4*>(&qc[g][l16 * 16]);
-        int dot = __dp4a(w.x, q.x, 0);
-        dot = __dp4a(w.y, q.y, dot);
-        dot = __dp4a(w.z, q.z, dot);
-        dot = __dp4a(w.w, q.w, dot);
+    const int mine = l16 % GP;          // the head whose total comes here
+    const double my_qs = qs[mine];
+    // one head: its codes stay in registers
+    int4 q1 = make_int4(0, 0, 0, 0);
+    if (GP == 1) q1 = *reinterpret_cast<const int4*>(&qc[0][l16 * 16]);
+    for (int i = warp * 2; i < n; i += kSelWarps * 2 * kSelFlight) {
+      int4 w[kSelFlight];
+      float s[kSelFlight];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-          dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float v =
-            float(__dmul_rn(__dmul_rn(double(dot), double(s)), qs[g]));
-        best = max_nan(best, v);
+      for (int f = 0; f < kSelFlight; ++f) {
+        const int blk = i + f * kSelWarps * 2 + (lane >> 4);
+        w[f] = make_int4(0, 0, 0, 0);
+        s[f] = 0.f;
+        if (blk < n) {
+          w[f] = __ldg(reinterpret_cast<const int4*>(
+              bounds + int64_t(blk) * (2 * kHeadDim)));
+          s[f] = __ldg(ks + blk);
+        }
       }
-      if (on && l16 == 0) score[blk] = best;
+#pragma unroll
+      for (int f = 0; f < kSelFlight; ++f) {
+        const int blk = i + f * kSelWarps * 2 + (lane >> 4);
+        if (i + f * kSelWarps * 2 >= n) break;
+        int dot[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          const int4 q = GP == 1 ? q1
+                                 : *reinterpret_cast<const int4*>(
+                                       &qc[g][l16 * 16]);
+          dot[g] = __dp4a(w[f].x, q.x, 0);
+          dot[g] = __dp4a(w[f].y, q.y, dot[g]);
+          dot[g] = __dp4a(w[f].z, q.z, dot[g]);
+          dot[g] = __dp4a(w[f].w, q.w, dot[g]);
+        }
+        const int total = sum16<GP>(dot);
+        // lanes whose head does not exist repeat the first one's
+        float v = float(
+            __dmul_rn(__dmul_rn(double(total), double(s[f])), my_qs));
+        if (GP > 1 && mine >= a.G) v = -INFINITY;
+#pragma unroll
+        for (int o = GP / 2; o > 0; o >>= 1)
+          v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (l16 == 0 && blk < n) score[blk] = v;
+      }
     }
   }
   __syncthreads();
@@ -195,31 +261,49 @@ kv8_select_kernel(const Kv8SelectArgs a, int C) {
     uint32_t prefix = 0, mask = 0;
     uint32_t left = uint32_t(a.K);
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
+    for (int pass = 0; pass < kSelPasses; ++pass) {
+      const int bits = pass < 2 ? 11 : 10;
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = (1u << bits) - 1u;
       for (int i = t; i < n; i += kSelThreads) {
         const uint32_t key = rank_key(score[i], forced(i));
         if ((key & mask) == prefix)
-          atomicAdd(&hist[pass][(key >> shift) & 255u], 1u);
+          atomicAdd(&hist[pass][(key >> shift) & digit], 1u);
       }
       if (C > 1) cluster_sync(); else __syncthreads();
-      // thread t counts bin 255 - t over the cluster: best bins first
-      uint32_t cnt = 0;
-      const int bin = kSelBins - 1 - t;
+      // thread t counts four digits over the cluster, the largest first
+      static_assert(kSelBins == 4 * kSelThreads, "digits per thread");
+      const int d0 = kSelBins - 4 - 4 * t;
+      uint4 cnt = make_uint4(0, 0, 0, 0);
       if (C > 1) {
-        for (int c = 0; c < C; ++c) cnt += peer_load(&hist[pass][bin], c);
+        uint4 x[kSelMost];
+#pragma unroll
+        for (int c = 0; c < kSelMost; ++c)
+          x[c] = c < C ? peer_load4(&hist[pass][d0], c)
+                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kSelMost; ++c) {
+          cnt.x += x[c].x; cnt.y += x[c].y;
+          cnt.z += x[c].z; cnt.w += x[c].w;
+        }
       } else {
-        cnt = hist[pass][bin];
+        cnt = *reinterpret_cast<const uint4*>(&hist[pass][d0]);
       }
       uint32_t total;
-      const uint2 pr = block_prefix(cnt, scan, &total);
-      if (pr.x < left && left <= pr.y) {
-        pick[0] = uint32_t(bin);
-        pick[1] = left - pr.x;
+      uint32_t before =
+          block_prefix(cnt.x + cnt.y + cnt.z + cnt.w, scan, &total);
+      const uint32_t c4[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (before < left && left <= before + c4[k]) {
+          pick[0] = uint32_t(d0 + 3 - k);
+          pick[1] = left - before;
+        }
+        before += c4[k];
       }
       __syncthreads();
       prefix |= pick[0] << shift;
-      mask |= 255u << shift;
+      mask |= digit << shift;
       left = pick[1];
       __syncthreads();
     }
@@ -228,52 +312,55 @@ kv8_select_kernel(const Kv8SelectArgs a, int C) {
   }
 
   // how many each CTA lists, then the lists in ascending order
-  uint32_t above = 0, equal = 0;
-  if (t < 2) counts[t] = 0;
-  __syncthreads();
-  for (int i = t; i < n; i += kSelThreads) {
-    if (all) {
-      ++above;
-    } else {
-      const uint32_t key = rank_key(score[i], forced(i));
-      above += key > bar;
-      equal += key == bar;
-    }
-  }
-  if (above) atomicAdd(&counts[0], above);
-  if (equal) atomicAdd(&counts[1], equal);
-  if (C > 1) cluster_sync(); else __syncthreads();
+  auto takes = [&](int k) -> uint32_t {  // 1: above the bar, 1 << 16: at it
+    if (k >= n) return 0u;
+    if (all) return 1u;
+    const uint32_t key = rank_key(score[k], forced(k));
+    return key > bar ? 1u : key == bar ? 1u << 16 : 0u;
+  };
   uint32_t at = 0, eq_before = 0;
-  for (int c = 0; c < r; ++c) {
-    at += peer_load(&counts[0], c);
-    eq_before += peer_load(&counts[1], c);
+  if (C > 1) {
+    uint32_t above = 0, equal = 0;
+    for (int i = t; i < n; i += kSelThreads) {
+      const uint32_t x = takes(i);
+      above += x & 0xffffu;
+      equal += x >> 16;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      if (above) atomicAdd(&counts[0], above);
+      if (equal) atomicAdd(&counts[1], equal);
+    }
+    cluster_sync();
+    uint4 x[kSelMost];
+#pragma unroll
+    for (int c = 0; c < kSelMost; ++c)
+      x[c] = c < r ? peer_load4(counts, c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < kSelMost; ++c) {
+      at += x[c].x;
+      eq_before += x[c].y;
+    }
+    // no CTA leaves while another may still read its counts; the wait
+    // for that comes after the list
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   at += min(eq_before, quota);
   uint32_t eq_left = quota - min(eq_before, quota);
   int32_t* blocks = a.blocks + bh * a.K;
   float* out_s = a.scores + bh * a.K;
   for (int i = 0; i < n; i += kSelThreads) {
-    const int k = i + t;
-    bool gt = false, eq = false;
-    if (k < n) {
-      if (all) {
-        gt = true;
-      } else {
-        const uint32_t key = rank_key(score[k], forced(k));
-        gt = key > bar;
-        eq = key == bar;
-      }
+    const uint32_t x = takes(i + t);
+    uint32_t total;
+    const uint32_t pre = block_prefix(x, scan, &total);
+    if ((x & 1u) || (x && (pre >> 16) < eq_left)) {
+      const uint32_t to = at + (pre & 0xffffu) + min(pre >> 16, eq_left);
+      blocks[to] = j0 + i0 + i + t;
+      out_s[to] = score[i + t];
     }
-    uint32_t n_eq, n_take;
-    const uint2 pe = block_prefix(eq ? 1u : 0u, scan, &n_eq);
-    const bool take = gt || (eq && pe.x < eq_left);
-    const uint2 pt = block_prefix(take ? 1u : 0u, scan, &n_take);
-    if (take) {
-      blocks[at + pt.x] = j0 + i0 + k;
-      out_s[at + pt.x] = score[k];
-    }
-    at += n_take;
-    eq_left -= min(eq_left, n_eq);
+    at += (total & 0xffffu) + min(total >> 16, eq_left);
+    eq_left -= min(total >> 16, eq_left);
   }
   // the rest of a short list
   if (r == 0)
@@ -281,19 +368,18 @@ kv8_select_kernel(const Kv8SelectArgs a, int C) {
       blocks[i] = -1;
       out_s[i] = -INFINITY;
     }
-  // no CTA leaves while another may still read its counts
-  if (C > 1) cluster_sync();
+  if (C > 1)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-}  // namespace
-
-cudaError_t launch_kv8_select(const Kv8SelectArgs& a, cudaStream_t st) {
+template <int GP>
+cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
   int C = 1;
-  while (C < 8 && nblk > 128 * C) C *= 2;
+  while (C < kSelMost && nblk > 256 * C) C *= 2;
   const int64_t grid = int64_t(a.B) * a.H * C;
   const size_t smem = size_t((nblk + C - 1) / C) * sizeof(float);
-  cudaError_t e = allow_smem<kv8_select_kernel>(int(smem));
+  cudaError_t e = allow_smem<kv8_select_kernel<GP>>(int(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
@@ -309,7 +395,17 @@ cudaError_t launch_kv8_select(const Kv8SelectArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, a, C);
+  return cudaLaunchKernelEx(&cfg, kv8_select_kernel<GP>, a, C);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_select(const Kv8SelectArgs& a, cudaStream_t st) {
+  const cudaError_t e = a.G == 1   ? launch_group<1>(a, st)
+                        : a.G == 2 ? launch_group<2>(a, st)
+                        : a.G <= 4 ? launch_group<4>(a, st)
+                        : a.G <= 8 ? launch_group<8>(a, st)
+                                   : launch_group<16>(a, st);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
