@@ -494,7 +494,7 @@ LWM_API int lwm_kv8_read(const void* k_cache, const void* v_cache,
  * to fp32; of the query heads that share a cache head the largest. The
  * first n_sink and the last n_recent visible blocks are always listed
  * (n_sink + n_recent <= n_select), then blocks whose score is NaN; ties go
- * to the lowest index. L <= 2^25. Async on stream. */
+ * to the lowest index. L <= 2^22. Async on stream. */
 LWM_API int lwm_kv8_select(const void* q, const int8_t* k_bounds,
                            const float* k_scale, const int32_t* kv_start,
                            const int32_t* kv_len, const int32_t* q_pos,

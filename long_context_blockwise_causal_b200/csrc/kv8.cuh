@@ -56,8 +56,8 @@ struct Kv8SelectArgs {
   int max_pos, B, L, H, G, K, n_sink, n_recent;
   bool half;
 };
-// Largest L: the scores of a row's blocks stay in a cluster's shared memory.
-constexpr int kKv8SelectMaxLen = 1 << 25;
+// Largest L: the scores of a row's blocks stay in one CTA's shared memory.
+constexpr int kKv8SelectMaxLen = 1 << 22;
 cudaError_t launch_kv8_select(const Kv8SelectArgs& a, cudaStream_t st);
 
 struct Kv8DecodeArgs {

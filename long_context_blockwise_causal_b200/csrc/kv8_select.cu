@@ -18,40 +18,37 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPasses = 3;                // digits of 11, 11 and 10 bits
+constexpr int kSelPasses = 3;                // digits of up to 11 bits
 constexpr int kSelBins = 2048;
 constexpr int kSelFlight = 4;                // pairs of blocks in flight
 constexpr int kSelMost = 8;                  // CTAs per cluster
+static_assert(kKv8SelectMaxLen / kKv8Block * 4 <= 160 * 1024,
+              "a row's scores fit one CTA's shared memory");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-// Four words of CTA `rank`'s shared memory, from the place where this CTA
-// has them.
-__device__ __forceinline__ uint4 peer_load4(const uint32_t* p, uint32_t rank) {
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores to the cluster's first CTA, where this CTA would have *p.
+__device__ __forceinline__ void first_store(const float* p, float v) {
   uint32_t at;
-  uint4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
                : "=r"(at)
-               : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at)
+               : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v)
                : "memory");
-  return v;
 }
 
-// Ranking order as an unsigned word: forced blocks, NaN, then by score.
-__device__ __forceinline__ uint32_t rank_key(float s, bool forced) {
-  if (forced) return 0xffffffffu;
-  if (s != s) return 0xfffffffeu;
+// Ranking order as an unsigned word: by score, NaN above all.
+__device__ __forceinline__ uint32_t rank_key(float s) {
+  if (s != s) return 0xff800001u;
   const uint32_t u = __float_as_uint(s + 0.f);   // -0 ranks as +0
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
@@ -103,20 +100,23 @@ __device__ __forceinline__ int sum16(int (&v)[GP]) {
   return v[0];
 }
 
-// A cluster of C CTAs per (row, cache head); CTA r scores the r-th share of
-// the visible blocks into its shared memory, and the cluster finds the K-th
-// best key by three rounds of digit counting over all its shares. Bound by
-// reading the bounds (256 bytes per block): 16 lanes share a block, a warp
-// keeps 4 pairs of blocks in flight. GP: G rounded up to a power of two.
+// A cluster of C CTAs per (row, cache head). CTA r scores the r-th share of
+// the visible blocks into the shared memory of the first CTA, which finds
+// the K-th best key by three rounds of digit counting and writes the list;
+// counting over the shares of all CTAs cost more in exchanges (23 us for
+// three rounds over 8 CTAs) than one CTA takes for everything. Scoring is
+// bound by reading the bounds (256 bytes per block): 16 lanes share a block,
+// a warp keeps 4 pairs of blocks in flight, the first of them while the
+// query is made ready. GP: G rounded up to a power of two.
 template <int GP>
 __global__ void __launch_bounds__(kSelThreads, 2)
 kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
-  extern __shared__ float score[];                    // [share]
+  extern __shared__ float score[];                    // [visible blocks]
   __shared__ __align__(16) int8_t qc[GP][2 * kHeadDim];
   __shared__ double qs[GP];
   __shared__ __align__(16) uint32_t hist[kSelPasses][kSelBins];
-  __shared__ __align__(16) uint32_t counts[4];        // above, equal
   __shared__ uint32_t scan[kSelWarps];
+  __shared__ uint2 runs[kSelWarps], span[kSelWarps];
   __shared__ uint32_t pick[2];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = int(cluster_rank());
@@ -124,7 +124,8 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   const int b = int(bh / a.H), h = int(bh - int64_t(b) * a.H);
   for (int i = t; i < kSelPasses * kSelBins; i += kSelThreads)
     hist[0][i] = 0;
-  if (t < 4) counts[t] = 0;
+  // a CTA that has arrived is running: its memory may be written
+  if (C > 1) cluster_arrive();
   pdl_wait();
   pdl_trigger();
 
@@ -136,6 +137,28 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   const int share = (nv + C - 1) / C;
   const int i0 = min(r * share, nv), n = min(share, nv - i0);
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
+
+  const int l16 = lane & 15;
+  const int8_t* bounds =
+      a.k_bounds + (bh * nblk + j0 + i0) * (2 * kHeadDim) + l16 * 16;
+  const float* ks = a.k_scale + bh * nblk + j0 + i0;
+  int4 w[kSelFlight];
+  float s[kSelFlight];
+  // blocks i, i + 1 (one per half warp) and those of the next flights
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int f = 0; f < kSelFlight; ++f) {
+      const int blk = i + f * kSelWarps * 2 + (lane >> 4);
+      w[f] = make_int4(0, 0, 0, 0);
+      s[f] = 0.f;
+      if (blk < n) {
+        w[f] = __ldg(reinterpret_cast<const int4*>(
+            bounds + int64_t(blk) * (2 * kHeadDim)));
+        s[f] = __ldg(ks + blk);
+      }
+    }
+  };
+  fetch(warp * 2);
 
   // query codes: qc[g] = (min(qi, 0), max(qi, 0)), as the bounds lie; a warp
   // per head, two pairs of the rotation per lane
@@ -196,32 +219,17 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
     if (lane == 0) qs[g] = bad ? 0.0 : __dmul_rn(m, 1.0 / 127.0);
   }
   __syncthreads();
+  if (C > 1) cluster_wait();
 
   // scores: 16 lanes per block, 16 of its 256 bounds each
   {
-    const int l16 = lane & 15;
-    const int8_t* bounds =
-        a.k_bounds + (bh * nblk + j0 + i0) * (2 * kHeadDim) + l16 * 16;
-    const float* ks = a.k_scale + bh * nblk + j0 + i0;
     const int mine = l16 % GP;          // the head whose total comes here
     const double my_qs = qs[mine];
     // one head: its codes stay in registers
     int4 q1 = make_int4(0, 0, 0, 0);
     if (GP == 1) q1 = *reinterpret_cast<const int4*>(&qc[0][l16 * 16]);
     for (int i = warp * 2; i < n; i += kSelWarps * 2 * kSelFlight) {
-      int4 w[kSelFlight];
-      float s[kSelFlight];
-#pragma unroll
-      for (int f = 0; f < kSelFlight; ++f) {
-        const int blk = i + f * kSelWarps * 2 + (lane >> 4);
-        w[f] = make_int4(0, 0, 0, 0);
-        s[f] = 0.f;
-        if (blk < n) {
-          w[f] = __ldg(reinterpret_cast<const int4*>(
-              bounds + int64_t(blk) * (2 * kHeadDim)));
-          s[f] = __ldg(ks + blk);
-        }
-      }
+      if (i > warp * 2) fetch(i);
 #pragma unroll
       for (int f = 0; f < kSelFlight; ++f) {
         const int blk = i + f * kSelWarps * 2 + (lane >> 4);
@@ -245,131 +253,137 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
 #pragma unroll
         for (int o = GP / 2; o > 0; o >>= 1)
           v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if (l16 == 0 && blk < n) score[blk] = v;
+        if (l16 == 0 && blk < n) {
+          if (r == 0)
+            score[blk] = v;
+          else
+            first_store(score + i0 + blk, v);
+        }
       }
     }
   }
-  __syncthreads();
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (r > 0) return;
+  } else {
+    __syncthreads();
+  }
 
-  auto forced = [&](int i) {      // i: index among this CTA's blocks
-    const int k = i0 + i;
-    return k < a.n_sink || k >= nv - a.n_recent;
-  };
+  // forced blocks are listed whatever they score
+  const int first_free = min(a.n_sink, nv);
+  const int last_free = max(first_free, nv - min(a.n_recent, nv));
   uint32_t bar = 0, quota = 0;    // take keys above bar, quota equal to it
   const bool all = nv <= a.K;
   if (!all) {
-    uint32_t prefix = 0, mask = 0;
-    uint32_t left = uint32_t(a.K);
-#pragma unroll 1
-    for (int pass = 0; pass < kSelPasses; ++pass) {
-      const int bits = pass < 2 ? 11 : 10;
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digit = (1u << bits) - 1u;
-      for (int i = t; i < n; i += kSelThreads) {
-        const uint32_t key = rank_key(score[i], forced(i));
-        if ((key & mask) == prefix)
-          atomicAdd(&hist[pass][(key >> shift) & digit], 1u);
-      }
-      if (C > 1) cluster_sync(); else __syncthreads();
-      // thread t counts four digits over the cluster, the largest first
-      static_assert(kSelBins == 4 * kSelThreads, "digits per thread");
-      const int d0 = kSelBins - 4 - 4 * t;
-      uint4 cnt = make_uint4(0, 0, 0, 0);
-      if (C > 1) {
-        uint4 x[kSelMost];
-#pragma unroll
-        for (int c = 0; c < kSelMost; ++c)
-          x[c] = c < C ? peer_load4(&hist[pass][d0], c)
-                       : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < kSelMost; ++c) {
-          cnt.x += x[c].x; cnt.y += x[c].y;
-          cnt.z += x[c].z; cnt.w += x[c].w;
-        }
-      } else {
-        cnt = *reinterpret_cast<const uint4*>(&hist[pass][d0]);
-      }
-      uint32_t total;
-      uint32_t before =
-          block_prefix(cnt.x + cnt.y + cnt.z + cnt.w, scan, &total);
-      const uint32_t c4[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (before < left && left <= before + c4[k]) {
-          pick[0] = uint32_t(d0 + 3 - k);
-          pick[1] = left - before;
-        }
-        before += c4[k];
-      }
-      __syncthreads();
-      prefix |= pick[0] << shift;
-      mask |= digit << shift;
-      left = pick[1];
-      __syncthreads();
+    uint32_t left = uint32_t(a.K - first_free - (nv - last_free));
+    // the keys' range, so that its 2048 parts tell them apart
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    for (int i = first_free + t; i < last_free; i += kSelThreads) {
+      const uint32_t key = rank_key(score[i]);
+      lo = min(lo, key);
+      hi = max(hi, key);
     }
-    bar = prefix;
-    quota = left;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) span[warp] = make_uint2(lo, hi);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      lo = min(lo, span[w].x);
+      hi = max(hi, span[w].y);
+    }
+    if (left == 0) {
+      bar = 0xffffffffu;
+    } else {
+      // keys in [lo, lo + 2^bits) hold the one that is left-th from the top
+      int bits = 32 - __clz(hi - lo);
+#pragma unroll 1
+      for (int pass = 0; bits > 0; ++pass) {
+        const int shift = max(bits - 11, 0);
+        for (int i = first_free + t; i < last_free; i += kSelThreads) {
+          const uint32_t d = (rank_key(score[i]) - lo) >> shift;
+          // keys outside the range do not count: those below it wrap around
+          // to 2^24 - 2 or more, as no two keys are further apart than
+          // 0xff000002, and a range below all of them has 21 bits at most
+          if (d < (1u << (bits - shift)))
+            atomicAdd(&hist[pass][d], 1u);
+        }
+        __syncthreads();
+        // thread t counts four digits, the largest first
+        static_assert(kSelBins == 4 * kSelThreads, "digits per thread");
+        const int d0 = kSelBins - 4 - 4 * t;
+        const uint4 cnt = *reinterpret_cast<const uint4*>(&hist[pass][d0]);
+        uint32_t total;
+        uint32_t before =
+            block_prefix(cnt.x + cnt.y + cnt.z + cnt.w, scan, &total);
+        const uint32_t c4[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (before < left && left <= before + c4[k]) {
+            pick[0] = uint32_t(d0 + 3 - k);
+            pick[1] = left - before;
+          }
+          before += c4[k];
+        }
+        __syncthreads();
+        lo += pick[0] << shift;
+        left = pick[1];
+        bits = shift;
+        __syncthreads();
+      }
+      bar = lo;
+      quota = left;
+    }
   }
 
-  // how many each CTA lists, then the lists in ascending order
-  auto takes = [&](int k) -> uint32_t {  // 1: above the bar, 1 << 16: at it
-    if (k >= n) return 0u;
-    if (all) return 1u;
-    const uint32_t key = rank_key(score[k], forced(k));
-    return key > bar ? 1u : key == bar ? 1u << 16 : 0u;
+  // The list in ascending order: warp w takes the w-th run of blocks, counts
+  // its keys above the bar and at it, and places them behind the runs before.
+  auto takes = [&](int k) -> uint32_t {   // 1: above the bar, 2: at it
+    if (k >= nv) return 0u;
+    if (all || k < first_free || k >= last_free) return 1u;
+    const uint32_t key = rank_key(score[k]);
+    return key > bar ? 1u : key == bar ? 2u : 0u;
   };
-  uint32_t at = 0, eq_before = 0;
-  if (C > 1) {
-    uint32_t above = 0, equal = 0;
-    for (int i = t; i < n; i += kSelThreads) {
-      const uint32_t x = takes(i);
-      above += x & 0xffffu;
-      equal += x >> 16;
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if (lane == 0) {
-      if (above) atomicAdd(&counts[0], above);
-      if (equal) atomicAdd(&counts[1], equal);
-    }
-    cluster_sync();
-    uint4 x[kSelMost];
-#pragma unroll
-    for (int c = 0; c < kSelMost; ++c)
-      x[c] = c < r ? peer_load4(counts, c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int c = 0; c < kSelMost; ++c) {
-      at += x[c].x;
-      eq_before += x[c].y;
-    }
-    // no CTA leaves while another may still read its counts; the wait
-    // for that comes after the list
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int run = (nv + kSelThreads - 1) / kSelThreads * 32;
+  const int k0 = warp * run, k1 = min(k0 + run, nv);
+  uint32_t above = 0, equal = 0;
+  for (int k = k0; k < k1; k += 32) {
+    const uint32_t x = takes(k + lane);
+    above += __popc(__ballot_sync(0xffffffffu, x == 1u));
+    equal += __popc(__ballot_sync(0xffffffffu, x == 2u));
   }
-  at += min(eq_before, quota);
-  uint32_t eq_left = quota - min(eq_before, quota);
+  if (lane == 0) {
+    runs[warp].x = above;
+    runs[warp].y = equal;
+  }
+  __syncthreads();
+  uint32_t at = 0, eq = 0;
+  for (int w = 0; w < warp; ++w) {
+    at += runs[w].x;
+    eq += runs[w].y;
+  }
   int32_t* blocks = a.blocks + bh * a.K;
   float* out_s = a.scores + bh * a.K;
-  for (int i = 0; i < n; i += kSelThreads) {
-    const uint32_t x = takes(i + t);
-    uint32_t total;
-    const uint32_t pre = block_prefix(x, scan, &total);
-    if ((x & 1u) || (x && (pre >> 16) < eq_left)) {
-      const uint32_t to = at + (pre & 0xffffu) + min(pre >> 16, eq_left);
-      blocks[to] = j0 + i0 + i + t;
-      out_s[to] = score[i + t];
+  const uint32_t below = (1u << lane) - 1u;
+  for (int k = k0; k < k1; k += 32) {
+    const uint32_t x = takes(k + lane);
+    const uint32_t m1 = __ballot_sync(0xffffffffu, x == 1u);
+    const uint32_t m2 = __ballot_sync(0xffffffffu, x == 2u);
+    const uint32_t my_eq = eq + __popc(m2 & below);
+    if (x == 1u || (x == 2u && my_eq < quota)) {
+      const uint32_t to = at + __popc(m1 & below) + min(my_eq, quota);
+      blocks[to] = j0 + k + lane;
+      out_s[to] = score[k + lane];
     }
-    at += (total & 0xffffu) + min(total >> 16, eq_left);
-    eq_left -= min(total >> 16, eq_left);
+    at += __popc(m1);
+    eq += __popc(m2);
   }
   // the rest of a short list
-  if (r == 0)
-    for (int i = nv + t; i < a.K; i += kSelThreads) {
-      blocks[i] = -1;
-      out_s[i] = -INFINITY;
-    }
-  if (C > 1)
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = nv + t; i < a.K; i += kSelThreads) {
+    blocks[i] = -1;
+    out_s[i] = -INFINITY;
+  }
 }
 
 template <int GP>
@@ -378,7 +392,7 @@ cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
   int C = 1;
   while (C < kSelMost && nblk > 256 * C) C *= 2;
   const int64_t grid = int64_t(a.B) * a.H * C;
-  const size_t smem = size_t((nblk + C - 1) / C) * sizeof(float);
+  const size_t smem = size_t(nblk) * sizeof(float);
   cudaError_t e = allow_smem<kv8_select_kernel<GP>>(int(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -74,7 +74,7 @@ INV, UNS, WSP = ops.ERR_INVALID_ARG, ops.ERR_UNSUPPORTED, ops.ERR_WORKSPACE
     (select, {"sink": 2 ** 31 - 1, "recent": 2 ** 31 - 1}, INV),
     (select, {"max_pos": 0}, INV), (select, {"layout": 7}, INV),
     (select, {"Hq": 34}, UNS), (select, {"D": 64}, UNS),
-    (select, {"L": (1 << 25) + 1}, UNS), (select, {"dtype": 1}, UNS),
+    (select, {"L": (1 << 22) + 1}, UNS), (select, {"dtype": 1}, UNS),
     (select, {"B": 0, "q": None}, ops.OK), (select, {"Hq": 0}, ops.OK),
     (decode, {"q": None}, INV), (decode, {"vc": ODD}, INV),
     (decode, {"ws": None}, INV), (decode, {"blocks": OFF, "K": 1}, INV),
