@@ -12,15 +12,13 @@
 // among them always; then blocks whose score is NaN; ties go to the lowest
 // index.
 #include "kv8.cuh"
+#include "tc_kernels.cuh"
 
 namespace lwm {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelPasses = 3;                // digits of up to 11 bits
 constexpr int kSelBins = 2048;
-constexpr int kSelFlight = 4;                // pairs of blocks in flight
 constexpr int kSelMost = 8;                  // CTAs per cluster
 static_assert(kKv8SelectMaxLen / kKv8Block * 4 <= 160 * 1024,
               "a row's scores fit one CTA's shared memory");
@@ -53,9 +51,14 @@ __device__ __forceinline__ uint32_t rank_key(float s) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Sum of x over the threads before this one; *total: over all of them.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* buf,
-                                                 uint32_t* total) {
+__device__ __forceinline__ float key_score(uint32_t k) {
+  if (k == 0xff800001u) return __int_as_float(0x7fffffff);
+  return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+
+// Sum of x over the threads before this one.
+template <int Warps>
+__device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* buf) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t inc = x;
 #pragma unroll
@@ -65,15 +68,9 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* buf,
   }
   if (lane == 31) buf[warp] = inc;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  uint32_t before = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const uint32_t y = buf[w];
-    before += w < warp ? y : 0u;
-    all += y;
-  }
-  __syncthreads();
-  *total = all;
+  for (int w = 0; w < Warps; ++w) before += w < warp ? buf[w] : 0u;
   return before + inc - x;
 }
 
@@ -106,12 +103,23 @@ __device__ __forceinline__ int sum16(int (&v)[GP]) {
 // counting over the shares of all CTAs cost more in exchanges (23 us for
 // three rounds over 8 CTAs) than one CTA takes for everything. Scoring is
 // bound by reading the bounds (256 bytes per block): 16 lanes share a block,
-// a warp keeps 4 pairs of blocks in flight, the first of them while the
-// query is made ready. GP: G rounded up to a power of two.
-template <int GP>
-__global__ void __launch_bounds__(kSelThreads, 2)
+// a warp keeps several pairs of blocks in flight, the first of them while
+// the query is made ready. GP: G rounded up to a power of two.
+template <int GP, int Threads>
+struct Sel {
+  // 512 threads, one CTA per SM, for few long rows; 256 threads, four CTAs
+  // per SM, for many rows
+  static constexpr int kFlight = Threads == 512 ? 8 : 4;
+  static constexpr int kPerSm = Threads == 512 ? 1 : 4;
+};
+
+template <int GP, int Threads>
+__global__ void __launch_bounds__(Threads, Sel<GP, Threads>::kPerSm)
 kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
-  extern __shared__ float score[];                    // [visible blocks]
+  constexpr int kSelThreads = Threads;
+  constexpr int kSelWarps = Threads / 32;
+  constexpr int kSelFlight = Sel<GP, Threads>::kFlight;
+  extern __shared__ __align__(16) float score[];      // [visible blocks]
   __shared__ __align__(16) int8_t qc[GP][2 * kHeadDim];
   __shared__ double qs[GP];
   __shared__ __align__(16) uint32_t hist[kSelPasses][kSelBins];
@@ -270,20 +278,34 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
     __syncthreads();
   }
 
+  // scores become ranking keys, four per thread and step; past the last
+  // block lie keys of 0, below every score's
+  uint4* key4 = reinterpret_cast<uint4*>(score);
+  const int n4 = (nv + 3) / 4;
   // forced blocks are listed whatever they score
   const int first_free = min(a.n_sink, nv);
   const int last_free = max(first_free, nv - min(a.n_recent, nv));
+  uint32_t lo = 0xffffffffu, hi = 0u;   // the free keys' range
+  for (int i = t; i < n4; i += kSelThreads) {
+    const float4 f = reinterpret_cast<const float4*>(score)[i];
+    const float v[4] = {f.x, f.y, f.z, f.w};
+    uint32_t k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      k[j] = 4 * i + j < nv ? rank_key(v[j]) : 0u;
+      if (4 * i + j >= first_free && 4 * i + j < last_free) {
+        lo = min(lo, k[j]);
+        hi = max(hi, k[j]);
+      }
+    }
+    key4[i] = make_uint4(k[0], k[1], k[2], k[3]);
+  }
   uint32_t bar = 0, quota = 0;    // take keys above bar, quota equal to it
   const bool all = nv <= a.K;
-  if (!all) {
-    uint32_t left = uint32_t(a.K - first_free - (nv - last_free));
-    // the keys' range, so that its 2048 parts tell them apart
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int i = first_free + t; i < last_free; i += kSelThreads) {
-      const uint32_t key = rank_key(score[i]);
-      lo = min(lo, key);
-      hi = max(hi, key);
-    }
+  uint32_t left = uint32_t(max(0, a.K - first_free - (nv - last_free)));
+  if (!all && left == 0) bar = 0xffffffffu;
+  if (!all && left > 0) {
+    // the range's 2048 parts tell the keys apart
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) span[warp] = make_uint2(lo, hi);
@@ -293,91 +315,127 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
       lo = min(lo, span[w].x);
       hi = max(hi, span[w].y);
     }
-    if (left == 0) {
-      bar = 0xffffffffu;
-    } else {
-      // keys in [lo, lo + 2^bits) hold the one that is left-th from the top
-      int bits = 32 - __clz(hi - lo);
+    // keys in [lo, lo + 2^bits) hold the one that is left-th from the top
+    int bits = 32 - __clz(hi - lo);
 #pragma unroll 1
-      for (int pass = 0; bits > 0; ++pass) {
-        const int shift = max(bits - 11, 0);
-        for (int i = first_free + t; i < last_free; i += kSelThreads) {
-          const uint32_t d = (rank_key(score[i]) - lo) >> shift;
-          // keys outside the range do not count: those below it wrap around
-          // to 2^24 - 2 or more, as no two keys are further apart than
-          // 0xff000002, and a range below all of them has 21 bits at most
-          if (d < (1u << (bits - shift)))
-            atomicAdd(&hist[pass][d], 1u);
-        }
-        __syncthreads();
-        // thread t counts four digits, the largest first
-        static_assert(kSelBins == 4 * kSelThreads, "digits per thread");
-        const int d0 = kSelBins - 4 - 4 * t;
-        const uint4 cnt = *reinterpret_cast<const uint4*>(&hist[pass][d0]);
-        uint32_t total;
-        uint32_t before =
-            block_prefix(cnt.x + cnt.y + cnt.z + cnt.w, scan, &total);
-        const uint32_t c4[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
+    for (int pass = 0; bits > 0; ++pass) {
+      const int shift = max(bits - 11, 0);
+      const uint32_t parts = 1u << (bits - shift);
+      // keys outside the range do not count: those below it wrap around to
+      // 2^24 - 2 or more, as no two keys are further apart than 0xff000002,
+      // and a range below some of them has 21 bits at most
+      for (int i = t; i < n4; i += kSelThreads) {
+        const uint4 k = key4[i];
+        const uint32_t d[4] = {(k.x - lo) >> shift, (k.y - lo) >> shift,
+                               (k.z - lo) >> shift, (k.w - lo) >> shift};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (before < left && left <= before + c4[k]) {
-            pick[0] = uint32_t(d0 + 3 - k);
+        for (int j = 0; j < 4; ++j)
+          if (d[j] < parts && 4 * i + j >= first_free && 4 * i + j < last_free)
+            atomicAdd(&hist[pass][d[j]], 1u);
+      }
+      __syncthreads();
+      // a thread counts a run of digits, the largest first
+      constexpr int kRun = kSelBins / kSelThreads;
+      const uint4* bins = reinterpret_cast<const uint4*>(
+          &hist[pass][kSelBins - kRun * (t + 1)]);
+      uint32_t c[kRun], mine = 0;
+#pragma unroll
+      for (int j = 0; j < kRun / 4; ++j) {
+        const uint4 x = bins[j];
+        c[kRun - 1 - 4 * j] = x.x;
+        c[kRun - 2 - 4 * j] = x.y;
+        c[kRun - 3 - 4 * j] = x.z;
+        c[kRun - 4 - 4 * j] = x.w;
+      }
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) mine += c[j];
+      uint32_t before = block_prefix<kSelWarps>(mine, scan);
+      if (before < left && left <= before + mine) {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) {
+          if (before < left && left <= before + c[j]) {
+            pick[0] = uint32_t(kSelBins - kRun * t - 1 - j);
             pick[1] = left - before;
           }
-          before += c4[k];
+          before += c[j];
         }
-        __syncthreads();
-        lo += pick[0] << shift;
-        left = pick[1];
-        bits = shift;
-        __syncthreads();
       }
-      bar = lo;
-      quota = left;
+      __syncthreads();
+      lo += pick[0] << shift;
+      left = pick[1];
+      bits = shift;
+      __syncthreads();
     }
+    bar = lo;
+    quota = left;
+  } else {
+    __syncthreads();              // the keys are in place
   }
 
-  // The list in ascending order: warp w takes the w-th run of blocks, counts
-  // its keys above the bar and at it, and places them behind the runs before.
-  auto takes = [&](int k) -> uint32_t {   // 1: above the bar, 2: at it
-    if (k >= nv) return 0u;
-    if (all || k < first_free || k >= last_free) return 1u;
-    const uint32_t key = rank_key(score[k]);
-    return key > bar ? 1u : key == bar ? 2u : 0u;
+  // The list in ascending order: warp w takes the w-th run of blocks, four
+  // per lane, counts its keys above the bar and at it, and places them
+  // behind the runs before.
+  auto takes = [&](int i, bool (&gt)[4], bool (&eq)[4]) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (i < n4) x = key4[i];
+    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = 4 * i + j;
+      gt[j] = at < nv && (all || at < first_free || at >= last_free ||
+                          k[j] > bar);
+      eq[j] = at < nv && !gt[j] && k[j] == bar;
+    }
   };
-  const int run = (nv + kSelThreads - 1) / kSelThreads * 32;
-  const int k0 = warp * run, k1 = min(k0 + run, nv);
+  const int run = (n4 + kSelThreads - 1) / kSelThreads * 32;
+  const int i_lo = warp * run, i_hi = min(i_lo + run, n4);
   uint32_t above = 0, equal = 0;
-  for (int k = k0; k < k1; k += 32) {
-    const uint32_t x = takes(k + lane);
-    above += __popc(__ballot_sync(0xffffffffu, x == 1u));
-    equal += __popc(__ballot_sync(0xffffffffu, x == 2u));
+  for (int i = i_lo; i < i_hi; i += 32) {
+    bool gt[4], eq[4];
+    takes(i + lane, gt, eq);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      above += gt[j];
+      equal += eq[j];
+    }
   }
-  if (lane == 0) {
-    runs[warp].x = above;
-    runs[warp].y = equal;
-  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) runs[warp] = make_uint2(above, equal);
   __syncthreads();
-  uint32_t at = 0, eq = 0;
-  for (int w = 0; w < warp; ++w) {
-    at += runs[w].x;
-    eq += runs[w].y;
+  uint32_t at = 0, eq_at = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    at += w < warp ? runs[w].x : 0u;
+    eq_at += w < warp ? runs[w].y : 0u;
   }
   int32_t* blocks = a.blocks + bh * a.K;
   float* out_s = a.scores + bh * a.K;
   const uint32_t below = (1u << lane) - 1u;
-  for (int k = k0; k < k1; k += 32) {
-    const uint32_t x = takes(k + lane);
-    const uint32_t m1 = __ballot_sync(0xffffffffu, x == 1u);
-    const uint32_t m2 = __ballot_sync(0xffffffffu, x == 2u);
-    const uint32_t my_eq = eq + __popc(m2 & below);
-    if (x == 1u || (x == 2u && my_eq < quota)) {
-      const uint32_t to = at + __popc(m1 & below) + min(my_eq, quota);
-      blocks[to] = j0 + k + lane;
-      out_s[to] = score[k + lane];
+  for (int i = i_lo; i < i_hi; i += 32) {
+    bool gt[4], eq[4];
+    takes(i + lane, gt, eq);
+    uint32_t g0 = at, e0 = eq_at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, gt[j]);
+      const uint32_t me = __ballot_sync(0xffffffffu, eq[j]);
+      g0 += __popc(mg & below);
+      e0 += __popc(me & below);
+      at += __popc(mg);
+      eq_at += __popc(me);
     }
-    at += __popc(m1);
-    eq += __popc(m2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (gt[j] || (eq[j] && e0 < quota)) {
+        const uint32_t to = g0 + min(e0, quota);
+        blocks[to] = j0 + 4 * (i + lane) + j;
+        out_s[to] = key_score(reinterpret_cast<const uint32_t*>(
+            score)[4 * (i + lane) + j]);
+      }
+      g0 += gt[j];
+      e0 += eq[j];
+    }
   }
   // the rest of a short list
   for (int i = nv + t; i < a.K; i += kSelThreads) {
@@ -386,18 +444,16 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   }
 }
 
-template <int GP>
-cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
+template <int GP, int Threads>
+cudaError_t launch_rows(const Kv8SelectArgs& a, int C, cudaStream_t st) {
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
-  int C = 1;
-  while (C < kSelMost && nblk > 256 * C) C *= 2;
   const int64_t grid = int64_t(a.B) * a.H * C;
-  const size_t smem = size_t(nblk) * sizeof(float);
-  cudaError_t e = allow_smem<kv8_select_kernel<GP>>(int(smem));
+  const size_t smem = size_t(nblk + 3) / 4 * 16;
+  cudaError_t e = allow_smem<kv8_select_kernel<GP, Threads>>(int(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(Threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -409,7 +465,22 @@ cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kv8_select_kernel<GP>, a, C);
+  return cudaLaunchKernelEx(&cfg, kv8_select_kernel<GP, Threads>, a, C);
+}
+
+// Few (row, head) pairs: a cluster of large CTAs each, as long as there are
+// SMs for all of them at once and 128 blocks for each. Many pairs, or short
+// rows: one small CTA each, four to an SM.
+template <int GP>
+cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
+  const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
+  const int64_t pairs = int64_t(a.B) * a.H;
+  const int sms = sm_count();
+  int C = 1;
+  while (C < kSelMost && pairs * C * 2 <= sms && nblk > 128 * C) C *= 2;
+  return C > 1 || (nblk > 512 && pairs <= sms)
+             ? launch_rows<GP, 512>(a, C, st)
+             : launch_rows<GP, 256>(a, C, st);
 }
 
 }  // namespace
