@@ -74,14 +74,14 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t* buf) {
   return before + inc - x;
 }
 
-// Adds up GP values over the 16 lanes that share a block, halving the number
-// of values a lane holds while it can: lane l ends with the total of value
-// l mod GP (in v[0]).
-template <int GP>
-__device__ __forceinline__ int sum16(int (&v)[GP]) {
+// Adds up N values (a power of two, at most 16) over the 16 lanes that share
+// a block, halving the number of values a lane holds while it can: lane l
+// ends with the total of value l mod N.
+template <int N>
+__device__ __forceinline__ int sum16(int (&v)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = GP / 2; o > 0; o >>= 1) {
+  for (int o = N / 2; o > 0; o >>= 1) {
     // of 2 o values, those whose index has bit o go to the lanes that have it
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -92,7 +92,7 @@ __device__ __forceinline__ int sum16(int (&v)[GP]) {
     }
   }
 #pragma unroll
-  for (int o = GP; o < 16; o <<= 1)
+  for (int o = N; o < 16; o <<= 1)
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   return v[0];
 }
@@ -111,6 +111,9 @@ struct Sel {
   // per SM, for many rows
   static constexpr int kFlight = Threads == 512 ? 8 : 4;
   static constexpr int kPerSm = Threads == 512 ? 1 : 4;
+  // pairs whose sums are finished together: one step of fp64 serves all of
+  // them (scores are rounded from fp64, whose conversions are slow)
+  static constexpr int kJoint = 16 / GP < kFlight ? 16 / GP : kFlight;
 };
 
 template <int GP, int Threads>
@@ -151,19 +154,15 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
       a.k_bounds + (bh * nblk + j0 + i0) * (2 * kHeadDim) + l16 * 16;
   const float* ks = a.k_scale + bh * nblk + j0 + i0;
   int4 w[kSelFlight];
-  float s[kSelFlight];
   // blocks i, i + 1 (one per half warp) and those of the next flights
   auto fetch = [&](int i) {
 #pragma unroll
     for (int f = 0; f < kSelFlight; ++f) {
       const int blk = i + f * kSelWarps * 2 + (lane >> 4);
       w[f] = make_int4(0, 0, 0, 0);
-      s[f] = 0.f;
-      if (blk < n) {
+      if (blk < n)
         w[f] = __ldg(reinterpret_cast<const int4*>(
             bounds + int64_t(blk) * (2 * kHeadDim)));
-        s[f] = __ldg(ks + blk);
-      }
     }
   };
   fetch(warp * 2);
@@ -231,37 +230,44 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
 
   // scores: 16 lanes per block, 16 of its 256 bounds each
   {
-    const int mine = l16 % GP;          // the head whose total comes here
-    const double my_qs = qs[mine];
+    constexpr int kJoint = Sel<GP, Threads>::kJoint, kSums = kJoint * GP;
+    const int mine = l16 % GP;                 // the head and, of the pairs
+    const int my_pair = l16 % kSums / GP;      // finished together, the one
+    const double my_qs = qs[mine];             // whose total comes here
     // one head: its codes stay in registers
     int4 q1 = make_int4(0, 0, 0, 0);
     if (GP == 1) q1 = *reinterpret_cast<const int4*>(&qc[0][l16 * 16]);
     for (int i = warp * 2; i < n; i += kSelWarps * 2 * kSelFlight) {
       if (i > warp * 2) fetch(i);
 #pragma unroll
-      for (int f = 0; f < kSelFlight; ++f) {
-        const int blk = i + f * kSelWarps * 2 + (lane >> 4);
-        if (i + f * kSelWarps * 2 >= n) break;
-        int dot[GP];
+      for (int f0 = 0; f0 < kSelFlight; f0 += kJoint) {
+        const int first = i + f0 * kSelWarps * 2;
+        if (first >= n) break;
+        const int blk = first + my_pair * kSelWarps * 2 + (lane >> 4);
+        const float s = blk < n ? __ldg(ks + blk) : 0.f;
+        int dot[kSums];
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
           const int4 q = GP == 1 ? q1
                                  : *reinterpret_cast<const int4*>(
                                        &qc[g][l16 * 16]);
-          dot[g] = __dp4a(w[f].x, q.x, 0);
-          dot[g] = __dp4a(w[f].y, q.y, dot[g]);
-          dot[g] = __dp4a(w[f].z, q.z, dot[g]);
-          dot[g] = __dp4a(w[f].w, q.w, dot[g]);
+#pragma unroll
+          for (int f = 0; f < kJoint; ++f) {
+            const int4 x = w[f0 + f];
+            int d = __dp4a(x.x, q.x, 0);
+            d = __dp4a(x.y, q.y, d);
+            d = __dp4a(x.z, q.z, d);
+            dot[f * GP + g] = __dp4a(x.w, q.w, d);
+          }
         }
-        const int total = sum16<GP>(dot);
-        // lanes whose head does not exist repeat the first one's
+        const int total = sum16<kSums>(dot);
         float v = float(
-            __dmul_rn(__dmul_rn(double(total), double(s[f])), my_qs));
+            __dmul_rn(__dmul_rn(double(total), double(s)), my_qs));
         if (GP > 1 && mine >= a.G) v = -INFINITY;
 #pragma unroll
         for (int o = GP / 2; o > 0; o >>= 1)
           v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if (l16 == 0 && blk < n) {
+        if (l16 < kSums && mine == 0 && blk < n) {
           if (r == 0)
             score[blk] = v;
           else
