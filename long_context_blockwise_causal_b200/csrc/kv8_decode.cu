@@ -156,8 +156,9 @@ struct Dec {
   // shared memory, from a 1024-byte boundary
   static constexpr int kQBytes = kNq * kHeadDim;
   static constexpr int kPBytes = kNp * kKv8Block;
+  static constexpr int kStats = 4 * GP;      // floats: see stats below
   static constexpr int kSmall = 2 * kQBytes + 2 * kPBytes + 2048 +
-                                (2 * 4 + 2 + 4) * GP * 4;
+                                (2 * 4 + 2 + 4) * GP * 4 + 8 * kStats * 4;
   // two CTAs per SM: as many stages as half of 227 KB holds
   static constexpr int kStages = 3 * 2 * kTile + kSmall + 2048 <= 116000 ? 3
                                                                          : 2;
@@ -167,7 +168,8 @@ struct Dec {
   static constexpr int kMaxAt = kRingAt + kDecRing * int(sizeof(Tile));
   static constexpr int kQsAt = kMaxAt + 2 * 4 * GP * 4;
   static constexpr int kSumAt = kQsAt + 2 * GP * 4;
-  static constexpr int kBars = (kSumAt + 4 * GP * 4 + 15) / 16 * 16;
+  static constexpr int kStatsAt = (kSumAt + 4 * GP * 4 + 15) / 16 * 16;
+  static constexpr int kBars = kStatsAt + 4 * 2 * kStats * 4;
   static constexpr int bFull = 0, bEmpty = kStages, bTok = 2 * kStages,
                        bS = bTok + kDecRing, bP = bS + 2, bO = bP + 2,
                        bQ = bO + 2, bDone = bQ + 2, kNumBars = bDone + 1;
@@ -210,6 +212,21 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
           "=r"(r[15])
         : "r"(at));
+  }
+}
+
+// N floats that every thread of a warp reads.
+template <int N>
+__device__ __forceinline__ void lds(const float* p, float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
   }
 }
 
@@ -271,8 +288,11 @@ __device__ __forceinline__ uint32_t next_term(float& a, float& b) {
   } else {
     const uint32_t w = enc2_e4m3(a, b);
     const float2 f = dec2_e4m3(w);
-    a = (a - f.x) * kStep;
-    b = (b - f.y) * kStep;
+    // (x - f) 16, exact: f 16 and the difference are
+    const float2 r = fma2(make_float2(a, b), make_float2(kStep, kStep),
+                          make_float2(f.x * -kStep, f.y * -kStep));
+    a = r.x;
+    b = r.y;
     return w;
   }
 }
@@ -351,6 +371,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   float* wmax = reinterpret_cast<float*>(smem + C::kMaxAt);   // [2][4][GP]
   float* qscale = reinterpret_cast<float*>(smem + C::kQsAt);  // [2][GP]
   float* wsum = reinterpret_cast<float*>(smem + C::kSumAt);   // [4][GP]
+  float* stats = reinterpret_cast<float*>(smem + C::kStatsAt);
   volatile int* abort_word =
       reinterpret_cast<volatile int*>(smem + C::kTail + 4);
   auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
@@ -566,7 +587,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (lane == 0) mbar_arrive(bar(C::bQ + buf));
     };
 
-    float m[GP], l[GP], acc[GP], alpha[GP], beta[GP];
+    float l[GP], acc[GP];
+    // Lane g (mod GP) of every warp follows head g: its running maximum m
+    // and, per tile, what all threads need of it, passed on through the
+    // warp's own stats [tile parity][4][GP]: the tile's maximum, the factors
+    // of the sums so far and of the tile's, and the tile's for the values.
+    const int my_head = lane & (GP - 1);
+    float m = -INFINITY;
+    auto stats_of = [&](int i) {
+      return stats + (warp * 2 + (i & 1)) * C::kStats;
+    };
     bool pending = false;
     // a wait that gave up is agreed on at the next barrier of these warps,
     // so that none is left at a barrier alone
@@ -595,6 +625,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       const uint32_t at = my_tmem + 2 * C::kNq + (i & 1) * C::kNp;
 #pragma unroll
       for (int n = 0; n < C::kPTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
+      float al[GP], be[GP];
+      lds<GP>(stats_of(i) + GP, al);
+      lds<GP>(stats_of(i) + 3 * GP, be);
       tmem_wait_ld();
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
@@ -602,7 +635,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int n = C::kPTerms - 2; n >= 0; --n)
           o = fmaf(o, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
-        acc[g] = fmaf(o, beta[g], acc[g] * alpha[g]);
+        acc[g] = fmaf(o, be[g], acc[g] * al[g]);
       }
       tc_fence_before();
     };
@@ -615,9 +648,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       vs = vs_next;
       if (ok && !(nxt.flags & kEnd)) fetch(nxt);
       if (cur.flags & kFirst) {
+        m = -INFINITY;
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-          m[g] = -INFINITY;
           l[g] = 0.f;
           acc[g] = 0.f;
         }
@@ -628,7 +661,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         go = softmax_all(ok);
         if (!go) break;
       }
-      float al[GP], be[GP];
       if (live) {
         float s[GP];
         {
@@ -636,6 +668,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           uint32_t r[C::kQTerms][GP];
 #pragma unroll
           for (int n = 0; n < C::kQTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
+          float qs[GP];
+          lds<GP>(qscale + (seg & 1) * GP, qs);
           tmem_wait_ld();
           tc_fence_before();
           const bool seen = t >= cur.lo && t < cur.hi;
@@ -645,32 +679,48 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int n = C::kQTerms - 2; n >= 0; --n)
               x = fmaf(x, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
-            s[g] = seen ? x * (ks * qscale[(seg & 1) * GP + g])
-                        : -INFINITY;
+            s[g] = seen ? x * (ks * qs[g]) : -INFINITY;
           }
         }
         float* wm = wmax + (i & 1) * 4 * GP;
+        float mx = 0.f;
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
           const float x = warp_max(s[g]);
-          if (lane == 0) wm[warp * GP + g] = x;
+          mx = my_head == g ? x : mx;
         }
+        if (lane < GP) wm[warp * GP + lane] = mx;
         go = softmax_all(ok);
         if (!go) break;
-        float p[GP];
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          const float mt = fmaxf(fmaxf(wm[g], wm[GP + g]),
-                                 fmaxf(wm[2 * GP + g], wm[3 * GP + g]));
-          const float mn = fmaxf(m[g], mt);
+        {
+          const float mt = fmaxf(fmaxf(wm[my_head], wm[GP + my_head]),
+                                 fmaxf(wm[2 * GP + my_head],
+                                       wm[3 * GP + my_head]));
+          const float mn = fmaxf(m, mt);
           const float mu = mn == -INFINITY ? 0.f : mn;
-          al[g] = exp2f(m[g] - mu);
-          be[g] = exp2f(mt - mu);
-          p[g] = exp2f(s[g] - (mt == -INFINITY ? 0.f : mt));
-          m[g] = mn;
-          l[g] = fmaf(p[g], be[g], l[g] * al[g]);
-          p[g] *= C::kPScale;
-          be[g] *= vs * (1.f / C::kPScale);
+          const float al = ex2(m - mu), be = ex2(mt - mu);
+          m = mn;
+          if (lane < GP) {
+            float* st = stats_of(i) + lane;
+            st[0] = mt == -INFINITY ? 0.f : mt;
+            st[GP] = al;
+            st[2 * GP] = be;
+            st[3 * GP] = be * (vs * (1.f / C::kPScale));
+          }
+          __syncwarp();
+        }
+        float p[GP];
+        {
+          float mt[GP], al[GP], be[GP];
+          lds<GP>(stats_of(i), mt);
+          lds<GP>(stats_of(i) + GP, al);
+          lds<GP>(stats_of(i) + 2 * GP, be);
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            p[g] = ex2(s[g] - mt[g]);
+            l[g] = fmaf(p[g], be[g], l[g] * al[g]);
+            p[g] *= C::kPScale;
+          }
         }
         uint8_t* dst = smem + C::kP + (i & 1) * C::kPBytes;
 #pragma unroll
@@ -704,13 +754,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       // the product of the tile before ran meanwhile
       if (pending) add_o(i - 1, true);
       pending = live;
-      if (live) {
-#pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          alpha[g] = al[g];
-          beta[g] = be[g];
-        }
-      }
       if (cur.flags & kLast) {
         add_o(i, live);
         pending = false;
@@ -735,13 +778,12 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           if (cur.flags & kWhole) {
             static_cast<__nv_bfloat16*>(a.out)[(o0 + g) * kHeadDim + t] =
                 __float2bfloat16_rn(lt == 0.f ? 0.f : acc[g] / lt);
-            if (t == 0)
-              a.lse[o0 + g] =
-                  lt == 0.f ? -INFINITY : (m[g] + log2f(lt)) * kLn2;
+            if (t == g)
+              a.lse[o0 + g] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
           } else {
             rec[part_acc(a.G) + g * kHeadDim + t] = acc[g];
-            if (t == 0) {
-              rec[g] = m[g];
+            if (t == g) {
+              rec[g] = m;
               rec[a.G + g] = lt;
             }
           }
