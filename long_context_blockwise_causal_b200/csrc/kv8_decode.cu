@@ -119,11 +119,11 @@ __host__ __device__ constexpr int part_stride(int G) {
 // so what a term cannot hold is small against the tile's own sum, however
 // far the running maximum lies above it.
 //
-// Warps 0-3: thread t is slot t of S (scores, maximum, weights) and channel
-// t of O (accumulator). Warp 4 issues the products, warp 5 walks the tiles
-// and loads them by TMA. The products of one tile run while the softmax
-// works on the next: S, P and O are double buffered.
-constexpr int kDecThreads = 192;
+// Softmax warps: four per group of at most 8 heads; thread t of a group is slot
+// t of S (scores, maximum, weights) and channel t of O (accumulator). The
+// warp after them issues the products, the last one walks the tiles and
+// loads them by TMA. The products of one tile run while the softmax works
+// on the next: S, P and O are double buffered.
 constexpr int kDecRing = 8;              // tile descriptions
 constexpr uint64_t kDecWaitNs = 4000000000ull;
 constexpr int kTile = kKv8Block * kHeadDim;   // bytes of K or V of one tile
@@ -142,13 +142,17 @@ struct __align__(8) Tile {
 
 template <bool kInt8, int GP>
 struct Dec {
+  static constexpr int kGroups = GP > 8 ? 2 : 1;        // of softmax warps
+  static constexpr int kHeads = GP / kGroups;           // per group
+  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kPerSm = 2;                      // CTAs
   static constexpr int kQTerms = kInt8 ? 3 : 5;
   static constexpr int kPTerms = 3;
   static constexpr int kNq = (kQTerms * GP + 15) / 16 * 16;
   static constexpr int kNp = (kPTerms * GP + 15) / 16 * 16;
   static constexpr int kCols = 2 * kNq + 2 * kNp;
   static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-  static_assert(kCols <= 256, "two CTAs share the SM's 512 columns");
+  static_assert(kCols <= 256, "CTAs share the SM's 512 columns");
   // factor from one term to the next, and of the first term
   static constexpr float kStep = kInt8 ? 254.f : 16.f;
   static constexpr float kPScale = kInt8 ? 127.f : 256.f;
@@ -156,26 +160,38 @@ struct Dec {
   // shared memory, from a 1024-byte boundary
   static constexpr int kQBytes = kNq * kHeadDim;
   static constexpr int kPBytes = kNp * kKv8Block;
-  static constexpr int kStats = 4 * GP;      // floats: see stats below
-  static constexpr int kSmall = 2 * kQBytes + 2 * kPBytes + 2048 +
-                                (2 * 4 + 2 + 4) * GP * 4 + 8 * kStats * 4;
-  // two CTAs per SM: as many stages as half of 227 KB holds
-  static constexpr int kStages = 3 * 2 * kTile + kSmall + 2048 <= 116000 ? 3
-                                                                         : 2;
-  static constexpr int kQ = kStages * 2 * kTile;
-  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kStats = 4 * kHeads;  // floats: see stats below
+  static constexpr int kSmall = kQBytes + 2 * kPBytes + 448 +
+                                (2 * 4 + 2 + 4) * GP * 4 +
+                                kGroups * 8 * kStats * 4;
+  // as many tiles as the CTA's part of 227 KB holds, V with the odd one.
+  // With three stages, a K tile is refilled together with its V tile: the
+  // two then load side by side, 7.4 TB/s from a 1M-token cache, where
+  // refilling it as soon as its scores are done gave 7.1. With fewer, the
+  // earlier refill wins (16 heads, 16 x 32K: 300 against 320 us).
+  static constexpr int kRoom = 233472 / kPerSm - 2048 - kSmall;
+  static constexpr int kTiles = kRoom / kTile < 6 ? kRoom / kTile : 6;
+  static constexpr int kKStages = kTiles / 2, kVStages = kTiles - kKStages;
+  static constexpr bool kEarlyK = kKStages < 3;
+  static_assert(kKStages >= 2, "the next tile loads while one is worked on");
+  static constexpr int kV = kKStages * kTile;
+  static constexpr int kQ = kTiles * kTile;
+  static constexpr int kP = kQ + kQBytes;
   static constexpr int kRingAt = kP + 2 * kPBytes;
   static constexpr int kMaxAt = kRingAt + kDecRing * int(sizeof(Tile));
   static constexpr int kQsAt = kMaxAt + 2 * 4 * GP * 4;
   static constexpr int kSumAt = kQsAt + 2 * GP * 4;
   static constexpr int kStatsAt = (kSumAt + 4 * GP * 4 + 15) / 16 * 16;
-  static constexpr int kBars = kStatsAt + 4 * 2 * kStats * 4;
-  static constexpr int bFull = 0, bEmpty = kStages, bTok = 2 * kStages,
+  static constexpr int kBars = kStatsAt + kGroups * 4 * 2 * kStats * 4;
+  static constexpr int bKFull = 0, bKEmpty = kKStages, bVFull = 2 * kKStages,
+                       bVEmpty = bVFull + kVStages,
+                       bTok = bVEmpty + kVStages,
                        bS = bTok + kDecRing, bP = bS + 2, bO = bP + 2,
                        bQ = bO + 2, bDone = bQ + 2, kNumBars = bDone + 1;
   static constexpr int kTail = kBars + kNumBars * 8;  // tmem base, abort word
   static constexpr int kSmem = kTail + 16 + 1024;
-  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+  static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory per SM");
+  static_assert(kVStages + 2 < kDecRing, "descriptions outlive their tiles");
 };
 
 // Byte (row, col) of a K-major operand of 128-byte rows, 128-byte swizzle.
@@ -263,14 +279,14 @@ __device__ __forceinline__ float term_value(uint32_t w) {
   return kInt8 ? float(int(w)) : __uint_as_float(w);
 }
 
-// Barrier of the softmax warps; true if all of their threads said so.
-__device__ __forceinline__ bool softmax_all(bool mine) {
+// Barrier of a group of softmax warps; true if all its threads said so.
+__device__ __forceinline__ bool softmax_all(int id, bool mine) {
   uint32_t all;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "bar.red.and.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(all)
-      : "r"(uint32_t(mine))
+      : "r"(id), "r"(uint32_t(mine))
       : "memory");
   return all != 0;
 }
@@ -358,7 +374,8 @@ struct Walker {
 };
 
 template <bool kInt8, int GP>
-__global__ void __launch_bounds__(kDecThreads, 2)
+__global__ void __launch_bounds__(Dec<kInt8, GP>::kThreads,
+                                  Dec<kInt8, GP>::kPerSm)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ Kv8DecodeArgs a) {
@@ -375,23 +392,24 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   volatile int* abort_word =
       reinterpret_cast<volatile int*>(smem + C::kTail + 4);
   auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kMmaWarp = 4 * C::kGroups, kLoadWarp = kMmaWarp + 1;
 
   // set up while the kernel before this one may still run
-  if (t == 0) {
+  if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const bool by_warps = i >= C::bP && i < C::bP + 2;
       const bool by_warps_q = i >= C::bQ && i < C::bQ + 2;
-      mbar_init(bar(i), by_warps || by_warps_q ? 4 : 1);
+      mbar_init(bar(i), by_warps || by_warps_q ? 4 * C::kGroups : 1);
     }
     fence_mbar_init();
     *abort_word = 0;
   }
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     tmem_alloc(sbase + C::kTail, C::kTmem);
     tmem_relinquish();
   }
-  if (warp == 5 && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
@@ -406,7 +424,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   };
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
 
-  if (warp == 5) {
+  if (warp == kLoadWarp) {
     // ------------------------------------------------------ tiles and TMA
     Walker w;
     w.rows = Rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
@@ -421,30 +439,37 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     w.emitted = true;
     if (lane == 0) {
       if (w.u < w.u1) w.rt = row_tiles(w.rows, w.b);
+      auto load = [&](const CUtensorMap* map, int full, uint32_t at,
+                      const Tile& x) {
+        if (x.lo < x.hi) {
+          mbar_arrive_expect_tx(bar(full), kTile);
+          tma_load_3d(at, map, bar(full), 0, x.blk * kKv8Block,
+                      x.b * a.H + x.h);
+        } else {
+          mbar_arrive(bar(full));
+        }
+      };
+      auto load_v = [&](int i, const Tile& x) {
+        const int s = i % C::kVStages;
+        if (i >= C::kVStages && !wait(C::bVEmpty + s, i / C::kVStages - 1))
+          return false;
+        load(&tm_v, C::bVFull + s, sbase + C::kV + s * kTile, x);
+        return true;
+      };
       Tile cur, nxt;
-      bool more = w.next(cur);
-      int i = 0;
-      bool ok = true;
+      bool more = w.next(cur), ok = true;
+      int i = 0, nv = 0;
       for (; more && ok; ++i) {
-        const int s = i % C::kStages;
-        const bool live = cur.lo < cur.hi;
-        const int64_t bh = int64_t(cur.b) * a.H + cur.h;
         more = w.next(nxt);
         if (!more || (nxt.flags & kFirst)) cur.flags |= kLast;
-        if (i >= C::kStages) ok = wait(C::bEmpty + s, i / C::kStages - 1);
+        const int s = i % C::kKStages;
+        if (i >= C::kKStages) ok = wait(C::bKEmpty + s, i / C::kKStages - 1);
         if (!ok) break;
-        if (live) {
-          const uint32_t at = sbase + s * 2 * kTile;
-          mbar_arrive_expect_tx(bar(C::bFull + s), 2 * kTile);
-          tma_load_3d(at, &tm_k, bar(C::bFull + s), 0, cur.blk * kKv8Block,
-                      int(bh));
-          tma_load_3d(at + kTile, &tm_v, bar(C::bFull + s), 0,
-                      cur.blk * kKv8Block, int(bh));
-        } else {
-          mbar_arrive(bar(C::bFull + s));
-        }
+        load(&tm_k, C::bKFull + s, sbase + s * kTile, cur);
         ring[i % kDecRing] = cur;
         mbar_arrive(bar(C::bTok + i % kDecRing));
+        ok = load_v(i, cur);
+        nv += ok;
         cur = nxt;
       }
       if (ok) {
@@ -452,11 +477,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         mbar_arrive(bar(C::bTok + i % kDecRing));
       }
       // no load is in flight when the CTA leaves, abandoned or not
-      for (int f = max(0, i - C::kStages); f < i; ++f)
-        mbar_wait(bar(C::bFull + f % C::kStages), (f / C::kStages) & 1,
+      for (int f = max(0, i - C::kKStages); f < i; ++f)
+        mbar_wait(bar(C::bKFull + f % C::kKStages), (f / C::kKStages) & 1,
+                  nullptr, a.status, kDecWaitNs);
+      for (int f = max(0, nv - C::kVStages); f < nv; ++f)
+        mbar_wait(bar(C::bVFull + f % C::kVStages), (f / C::kVStages) & 1,
                   nullptr, a.status, kDecWaitNs);
     }
-  } else if (warp == 4) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t idq = idesc8<kInt8>(C::kNq, 0);
@@ -468,33 +496,36 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int flags = ring[i % kDecRing].flags;
         if (flags & kEnd) return 1;
         const bool live = ring[i % kDecRing].lo < ring[i % kDecRing].hi;
-        const int s = i % C::kStages;
+        const int s = i % C::kKStages;
         if (flags & kFirst) {
           ++seg;
           if (!wait(C::bQ + (seg & 1), seg >> 1)) return 2;
         }
-        if (!wait(C::bFull + s, i / C::kStages)) return 2;
+        if (!wait(C::bKFull + s, i / C::kKStages)) return 2;
         tc_fence_after();
         if (live) {
-          const uint64_t kd = sdesc_sw128(sbase + s * 2 * kTile, 16, 1024);
+          const uint64_t kd = sdesc_sw128(sbase + s * kTile, 16, 1024);
           const uint64_t qd =
-              sdesc_sw128(sbase + C::kQ + (seg & 1) * C::kQBytes, 16, 1024);
+              sdesc_sw128(sbase + C::kQ, 16, 1024);
 #pragma unroll
           for (int k = 0; k < kHeadDim / 32; ++k)
             mma8<kInt8>(tmem + (i & 1) * C::kNq, kd + 2 * k, qd + 2 * k, idq,
                         k > 0);
         }
+        if (C::kEarlyK) mma_commit(bar(C::bKEmpty + s));
         mma_commit(bar(C::bS + (i & 1)));
         return 0;
       };
       // weights times values of tile i
       auto pv = [&](int i) {
-        if (!wait(C::bP + (i & 1), i >> 1)) return false;
+        const int s = i % C::kVStages;
+        if (!wait(C::bP + (i & 1), i >> 1) ||
+            !wait(C::bVFull + s, i / C::kVStages))
+          return false;
         tc_fence_after();
-        const int s = i % C::kStages;
         if (ring[i % kDecRing].lo < ring[i % kDecRing].hi) {
           const uint64_t vd =
-              sdesc_sw128(sbase + s * 2 * kTile + kTile, kTile, 1024);
+              sdesc_sw128(sbase + C::kV + s * kTile, kTile, 1024);
           const uint64_t pd =
               sdesc_sw128(sbase + C::kP + (i & 1) * C::kPBytes, 16, 1024);
 #pragma unroll
@@ -503,7 +534,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         vd + uint64_t(k * (32 * kHeadDim >> 4)), pd + 2 * k,
                         idp, k > 0);
         }
-        mma_commit(bar(C::bEmpty + s));
+        if (!C::kEarlyK) mma_commit(bar(C::bKEmpty + i % C::kKStages));
+        mma_commit(bar(C::bVEmpty + s));
         mma_commit(bar(C::bO + (i & 1)));
         return true;
       };
@@ -522,9 +554,15 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
   } else {
     // ------------------------------------------------------------- softmax
-    const uint32_t my_tmem = tmem + (uint32_t(warp * 32) << 16);
+    constexpr int GH = C::kHeads;         // this group's heads: h0 + g
+    const int t = threadIdx.x & 127, quad = warp & 3;
+    const int group = C::kGroups == 1 ? 0 : warp >> 2;
+    const int h0 = group * GH, sync_id = 1 + group;
+    const uint32_t my_tmem = tmem + (uint32_t(quad * 32) << 16) + h0;
     int seg = -1;
     // Query of a (row, head): rotated, split into terms, thread t channel t.
+    // Called when the scores of the (row, head) before are all done, so that
+    // the terms may overwrite its own; buf: which of two sets of scales.
     auto make_q = [&](int b, int h, int buf) {
       const int pos = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
       const int k = a.half ? (t & 63) : (t >> 1);
@@ -534,65 +572,66 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                               int64_t(pos) * (kHeadDim / 2) + k);
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
                                (int64_t(b) * a.H + h) * a.G * kHeadDim;
-      float x[GP];
+      float x[GH];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
+      for (int g = 0; g < GH; ++g) {
         x[g] = 0.f;
-        if (g < a.G) {
-          const float qa = __bfloat162float(q[g * kHeadDim + ia]);
-          const float qb = __bfloat162float(q[g * kHeadDim + ib]);
+        if (h0 + g < a.G) {
+          const float qa = __bfloat162float(q[(h0 + g) * kHeadDim + ia]);
+          const float qb = __bfloat162float(q[(h0 + g) * kHeadDim + ib]);
           x[g] = low ? qa * cs.x - qb * cs.y : qa * cs.y + qb * cs.x;
         }
       }
-      float big[GP];
+      float big[GH];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
+      for (int g = 0; g < GH; ++g) {
         // a NaN or an infinity counts as the largest magnitude
         const float m = fabsf(x[g]);
         big[g] = warp_max(m <= 3.402823466e38f ? m : INFINITY);
       }
       if (lane == 0)
 #pragma unroll
-        for (int g = 0; g < GP; ++g) wsum[warp * GP + g] = big[g];
-      named_barrier_sync(1, 128);
-      float y[GP];
+        for (int g = 0; g < GH; ++g) wsum[quad * GP + h0 + g] = big[g];
+      named_barrier_sync(sync_id, 128);
+      float y[GH];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float m = fmaxf(fmaxf(wsum[g], wsum[GP + g]),
-                              fmaxf(wsum[2 * GP + g], wsum[3 * GP + g]));
+      for (int g = 0; g < GH; ++g) {
+        const float* w = wsum + h0 + g;
+        const float m = fmaxf(fmaxf(w[0], w[GP]),
+                              fmaxf(w[2 * GP], w[3 * GP]));
         const bool fine = m <= 3.402823466e38f;
         // m < 2^e
         const int e = int(__float_as_uint(m) >> 23) - 126;
         y[g] = fine ? ldexpf(x[g], C::kQExp - e) : 0.f;
         if (t == 0)
-          qscale[buf * GP + g] =
+          qscale[buf * GP + h0 + g] =
               fine ? ldexpf(kLog2e / sqrtf(float(kHeadDim)), e - C::kQExp)
                    : __int_as_float(0x7fffffff);
       }
-      uint8_t* dst = smem + C::kQ + buf * C::kQBytes;
+      uint8_t* dst = smem + C::kQ;
 #pragma unroll
       for (int n = 0; n < C::kQTerms; ++n) {
 #pragma unroll
-        for (int g = 0; g < GP; g += 2) {
+        for (int g = 0; g < GH; g += 2) {
           float dummy = 0.f;
           const uint32_t w =
-              next_term<kInt8>(y[g], g + 1 < GP ? y[(g + 1) % GP] : dummy);
-          dst[sw128(n * GP + g, t)] = uint8_t(w);
-          if (g + 1 < GP) dst[sw128(n * GP + g + 1, t)] = uint8_t(w >> 8);
+              next_term<kInt8>(y[g], g + 1 < GH ? y[(g + 1) % GH] : dummy);
+          dst[sw128(n * GP + h0 + g, t)] = uint8_t(w);
+          if (g + 1 < GH) dst[sw128(n * GP + h0 + g + 1, t)] = uint8_t(w >> 8);
         }
       }
       fence_proxy_async_smem();
       // all of wsum has been read and qscale written before anyone goes on
-      named_barrier_sync(1, 128);
+      named_barrier_sync(sync_id, 128);
       if (lane == 0) mbar_arrive(bar(C::bQ + buf));
     };
 
-    float l[GP], acc[GP];
-    // Lane g (mod GP) of every warp follows head g: its running maximum m
+    float l[GH], acc[GH];
+    // Lane g (mod GH) of every warp follows head h0 + g: its running maximum m
     // and, per tile, what all threads need of it, passed on through the
-    // warp's own stats [tile parity][4][GP]: the tile's maximum, the factors
+    // warp's own stats [tile parity][4][GH]: the tile's maximum, the factors
     // of the sums so far and of the tile's, and the tile's for the values.
-    const int my_head = lane & (GP - 1);
+    const int my_head = lane & (GH - 1);
     float m = -INFINITY;
     auto stats_of = [&](int i) {
       return stats + (warp * 2 + (i & 1)) * C::kStats;
@@ -601,7 +640,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     // a wait that gave up is agreed on at the next barrier of these warps,
     // so that none is left at a barrier alone
     bool ok = wait(C::bTok, 0);
-    bool go = softmax_all(ok);
+    bool go = softmax_all(sync_id, ok);
     Tile cur = ring[0];
     // scales of a tile, fetched while the tile before it is worked on
     float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
@@ -621,16 +660,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       ok = wait(C::bO + (i & 1), i >> 1) && ok;
       if (!live) return;
       tc_fence_after();
-      uint32_t r[C::kPTerms][GP];
+      uint32_t r[C::kPTerms][GH];
       const uint32_t at = my_tmem + 2 * C::kNq + (i & 1) * C::kNp;
 #pragma unroll
-      for (int n = 0; n < C::kPTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
-      float al[GP], be[GP];
-      lds<GP>(stats_of(i) + GP, al);
-      lds<GP>(stats_of(i) + 3 * GP, be);
+      for (int n = 0; n < C::kPTerms; ++n) tmem_ld<GH>(at + n * GP, r[n]);
+      float al[GH], be[GH];
+      lds<GH>(stats_of(i) + GH, al);
+      lds<GH>(stats_of(i) + 3 * GH, be);
       tmem_wait_ld();
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
+      for (int g = 0; g < GH; ++g) {
         float o = term_value<kInt8>(r[C::kPTerms - 1][g]);
 #pragma unroll
         for (int n = C::kPTerms - 2; n >= 0; --n)
@@ -650,7 +689,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (cur.flags & kFirst) {
         m = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
+        for (int g = 0; g < GH; ++g) {
           l[g] = 0.f;
           acc[g] = 0.f;
         }
@@ -658,23 +697,23 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       ok = wait(C::bS + (i & 1), i >> 1) && ok;
       tc_fence_after();
       if (!live) {
-        go = softmax_all(ok);
+        go = softmax_all(sync_id, ok);
         if (!go) break;
       }
       if (live) {
-        float s[GP];
+        float s[GH];
         {
           const uint32_t at = my_tmem + (i & 1) * C::kNq;
-          uint32_t r[C::kQTerms][GP];
+          uint32_t r[C::kQTerms][GH];
 #pragma unroll
-          for (int n = 0; n < C::kQTerms; ++n) tmem_ld<GP>(at + n * GP, r[n]);
-          float qs[GP];
-          lds<GP>(qscale + (seg & 1) * GP, qs);
+          for (int n = 0; n < C::kQTerms; ++n) tmem_ld<GH>(at + n * GP, r[n]);
+          float qs[GH];
+          lds<GH>(qscale + (seg & 1) * GP + h0, qs);
           tmem_wait_ld();
           tc_fence_before();
           const bool seen = t >= cur.lo && t < cur.hi;
 #pragma unroll
-          for (int g = 0; g < GP; ++g) {
+          for (int g = 0; g < GH; ++g) {
             float x = term_value<kInt8>(r[C::kQTerms - 1][g]);
 #pragma unroll
             for (int n = C::kQTerms - 2; n >= 0; --n)
@@ -682,15 +721,15 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
             s[g] = seen ? x * (ks * qs[g]) : -INFINITY;
           }
         }
-        float* wm = wmax + (i & 1) * 4 * GP;
+        float* wm = wmax + (i & 1) * 4 * GP + h0;
         float mx = 0.f;
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
+        for (int g = 0; g < GH; ++g) {
           const float x = warp_max(s[g]);
           mx = my_head == g ? x : mx;
         }
-        if (lane < GP) wm[warp * GP + lane] = mx;
-        go = softmax_all(ok);
+        if (lane < GH) wm[quad * GP + lane] = mx;
+        go = softmax_all(sync_id, ok);
         if (!go) break;
         {
           const float mt = fmaxf(fmaxf(wm[my_head], wm[GP + my_head]),
@@ -700,23 +739,23 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           const float mu = mn == -INFINITY ? 0.f : mn;
           const float al = ex2(m - mu), be = ex2(mt - mu);
           m = mn;
-          if (lane < GP) {
+          if (lane < GH) {
             float* st = stats_of(i) + lane;
             st[0] = mt == -INFINITY ? 0.f : mt;
-            st[GP] = al;
-            st[2 * GP] = be;
-            st[3 * GP] = be * (vs * (1.f / C::kPScale));
+            st[GH] = al;
+            st[2 * GH] = be;
+            st[3 * GH] = be * (vs * (1.f / C::kPScale));
           }
           __syncwarp();
         }
-        float p[GP];
+        float p[GH];
         {
-          float mt[GP], al[GP], be[GP];
-          lds<GP>(stats_of(i), mt);
-          lds<GP>(stats_of(i) + GP, al);
-          lds<GP>(stats_of(i) + 2 * GP, be);
+          float mt[GH], al[GH], be[GH];
+          lds<GH>(stats_of(i), mt);
+          lds<GH>(stats_of(i) + GH, al);
+          lds<GH>(stats_of(i) + 2 * GH, be);
 #pragma unroll
-          for (int g = 0; g < GP; ++g) {
+          for (int g = 0; g < GH; ++g) {
             p[g] = ex2(s[g] - mt[g]);
             l[g] = fmaf(p[g], be[g], l[g] * al[g]);
             p[g] *= C::kPScale;
@@ -726,20 +765,20 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int n = 0; n < C::kPTerms; ++n) {
 #pragma unroll
-          for (int g = 0; g < GP; g += 2) {
+          for (int g = 0; g < GH; g += 2) {
             float dummy = 0.f;
             const uint32_t w =
-                next_term<kInt8>(p[g], g + 1 < GP ? p[(g + 1) % GP] : dummy);
-            dst[sw128(n * GP + g, t)] = uint8_t(w);
-            if (g + 1 < GP) dst[sw128(n * GP + g + 1, t)] = uint8_t(w >> 8);
+                next_term<kInt8>(p[g], g + 1 < GH ? p[(g + 1) % GH] : dummy);
+            dst[sw128(n * GP + h0 + g, t)] = uint8_t(w);
+            if (g + 1 < GH)
+              dst[sw128(n * GP + h0 + g + 1, t)] = uint8_t(w >> 8);
           }
         }
-        if (!kInt8 && (t < cur.lo || t >= cur.hi)) {
-          // an unseen slot's weight is 0, but its codes may be NaN (the
-          // tile is in place: its barrier has flipped, S came after it)
-          wait(C::bFull + i % C::kStages, i / C::kStages);
+        if (!kInt8 && group == 0 && (t < cur.lo || t >= cur.hi)) {
+          // an unseen slot's weight is 0, but its codes may be NaN
+          ok = wait(C::bVFull + i % C::kVStages, i / C::kVStages) && ok;
           uint4* row = reinterpret_cast<uint4*>(
-              smem + (i % C::kStages) * 2 * kTile + kTile + t * kHeadDim);
+              smem + C::kV + (i % C::kVStages) * kTile + t * kHeadDim);
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k)
             row[k] = make_uint4(0, 0, 0, 0);
@@ -758,37 +797,38 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         add_o(i, live);
         pending = false;
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
+        for (int g = 0; g < GH; ++g) {
           float x = l[g];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == 0) wsum[warp * GP + g] = x;
+          if (lane == 0) wsum[quad * GP + h0 + g] = x;
         }
-        named_barrier_sync(1, 128);
+        named_barrier_sync(sync_id, 128);
         const int64_t o0 = (int64_t(cur.b) * a.H + cur.h) * a.G;
         float* rec = a.part + (int64_t(blockIdx.x) * 2 +
                                ((cur.flags & kSlot1) ? 1 : 0)) *
                                   part_stride(a.G);
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          if (g >= a.G) break;
-          const float lt = (wsum[g] + wsum[GP + g]) +
-                           (wsum[2 * GP + g] + wsum[3 * GP + g]);
+        for (int g = 0; g < GH; ++g) {
+          const int hq = h0 + g;
+          if (hq >= a.G) break;
+          const float* w = wsum + hq;
+          const float lt = (w[0] + w[GP]) + (w[2 * GP] + w[3 * GP]);
           if (cur.flags & kWhole) {
-            static_cast<__nv_bfloat16*>(a.out)[(o0 + g) * kHeadDim + t] =
+            static_cast<__nv_bfloat16*>(a.out)[(o0 + hq) * kHeadDim + t] =
                 __float2bfloat16_rn(lt == 0.f ? 0.f : acc[g] / lt);
             if (t == g)
-              a.lse[o0 + g] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
+              a.lse[o0 + hq] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
           } else {
-            rec[part_acc(a.G) + g * kHeadDim + t] = acc[g];
+            rec[part_acc(a.G) + hq * kHeadDim + t] = acc[g];
             if (t == g) {
-              rec[g] = m;
-              rec[a.G + g] = lt;
+              rec[hq] = m;
+              rec[a.G + hq] = lt;
             }
           }
         }
-        named_barrier_sync(1, 128);   // wsum is free again
+        named_barrier_sync(sync_id, 128);   // wsum is free again
         ++seg;
       }
       cur = nxt;
@@ -796,7 +836,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
@@ -903,15 +943,17 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
 
 }  // namespace
 
-int kv8_decode_grid(int B, int L, int H, int K) {
-  // two CTAs per SM, never more than there can be tiles
+int kv8_decode_grid(int B, int L, int H, int G, int K) {
+  // every SM's CTAs at once, never more than there can be tiles
+  const int per_sm =
+      G > 8 ? Dec<false, 16>::kPerSm : Dec<false, 8>::kPerSm;
   const int64_t per = K >= 0 ? K : (L + kKv8Block - 1) / kKv8Block;
   const int64_t most = int64_t(B) * H * per;
-  return int(std::max<int64_t>(1, std::min<int64_t>(most, 2 * sm_count())));
+  return int(std::max<int64_t>(1, std::min<int64_t>(most, per_sm * sm_count())));
 }
 
 size_t kv8_part_floats(int B, int L, int H, int G, int K) {
-  return size_t(kv8_decode_grid(B, L, H, K)) * 2 * part_stride(G);
+  return size_t(kv8_decode_grid(B, L, H, G, K)) * 2 * part_stride(G);
 }
 
 namespace {
@@ -930,7 +972,7 @@ cudaError_t launch_tiles(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
   const cudaError_t e = allow_smem<kv8_decode_kernel<kInt8, GP>>(D::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv8_decode_kernel<kInt8, GP>, dim3(C),
-                          dim3(kDecThreads), D::kSmem, st, mk, mv, a);
+                          dim3(D::kThreads), D::kSmem, st, mk, mv, a);
 }
 
 template <bool kInt8>
@@ -945,7 +987,7 @@ cudaError_t launch_group(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
-  const int C = kv8_decode_grid(a.B, a.L, a.H, a.listed ? a.K : -1);
+  const int C = kv8_decode_grid(a.B, a.L, a.H, a.G, a.listed ? a.K : -1);
   cudaError_t e =
       a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;
