@@ -207,6 +207,10 @@ int lwm_kv8_decode(const void* q, const void* k_cache, const void* v_cache,
   s = query_status(Hq, H, max_pos, rope_layout);
   if (s != LWM_OK) return s;
   const bool listed = n_blocks >= 0;
+  // tiles (blocks of all rows and heads) are counted in 32 bits
+  const int64_t per = listed ? n_blocks : (int64_t(L) + kKv8Block - 1) / kKv8Block;
+  if (int64_t(B) * H * per >= (int64_t(1) << 31) - 4096)
+    return LWM_ERR_UNSUPPORTED;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
   if (int64_t(B) * Hq == 0) return LWM_OK;
   if (!wide_ok({q, rope_table, out, workspace}) ||

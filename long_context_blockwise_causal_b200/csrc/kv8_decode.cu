@@ -27,18 +27,24 @@ __device__ __forceinline__ float warp_max(float x) {
 struct Rows {
   const int32_t* kv_start;
   const int32_t* kv_len;
-  int B, L, H, K;
+  const int32_t* q_pos;
+  int max_pos, B, L, H, K;
   bool listed;
 };
 
+// Tiles are counted in 32 bits (the host refuses a call of more).
 struct RowTiles {
   int start, len, t0, n;    // visible slots, first block, tiles per head
+  int pos;                  // of the query
 };
 
 __device__ __forceinline__ RowTiles row_tiles(const Rows& r, int b) {
   RowTiles x;
-  x.len = max(0, min(__ldg(r.kv_len + b), r.L));
-  x.start = max(0, min(__ldg(r.kv_start + b), x.len));
+  const int len = __ldg(r.kv_len + b), start = __ldg(r.kv_start + b);
+  const int pos = __ldg(r.q_pos + b);
+  x.len = max(0, min(len, r.L));
+  x.start = max(0, min(start, x.len));
+  x.pos = max(0, min(pos, r.max_pos - 1));
   x.t0 = x.start / kKv8Block;
   x.n = x.len > x.start
             ? (r.listed ? r.K : (x.len + kKv8Block - 1) / kKv8Block - x.t0)
@@ -47,56 +53,76 @@ __device__ __forceinline__ RowTiles row_tiles(const Rows& r, int b) {
 }
 
 // A warp's lanes together: tiles per head of rows [0, upto).
-__device__ __forceinline__ int64_t tiles_before(const Rows& r, int upto) {
-  int64_t s = 0;
+__device__ __forceinline__ int tiles_before(const Rows& r, int upto) {
+  int s = 0;
   for (int b = threadIdx.x & 31; b < upto; b += 32) s += row_tiles(r, b).n;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// A warp's lanes together: the row that holds tile u (counted over all rows
-// and heads), and the tiles before that row.
-__device__ __forceinline__ int find_row(const Rows& r, int64_t u,
-                                        int64_t* before) {
-  const int lane = threadIdx.x & 31;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < r.B; b0 += 32) {
-    int64_t n = b0 + lane < r.B ? int64_t(row_tiles(r, b0 + lane).n) * r.H : 0;
-    int64_t inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, u < base + inc);
-    if (hit) {
-      const int f = __ffs(hit) - 1;
-      *before = base + __shfl_sync(0xffffffffu, inc - n, f);
-      return b0 + f;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  *before = base;
-  return r.B;
+  return __reduce_add_sync(0xffffffffu, s);
 }
 
 // CTA c of C takes tiles [first(c), first(c + 1)): the first `more` CTAs
 // take one tile more than the others.
 struct Shares {
-  int64_t each;
-  int more;
-  __device__ __forceinline__ Shares(int64_t total, int C)
-      : each(total / C), more(int(total - each * C)) {}
-  __device__ __forceinline__ int64_t first(int c) const {
+  int each, more;
+  __device__ __forceinline__ Shares(int total, int C)
+      : each(total / C), more(total - each * C) {}
+  __device__ __forceinline__ int first(int c) const {
     return each * c + min(c, more);
   }
   // The CTA that holds tile u.
-  __device__ __forceinline__ int holder(int64_t u) const {
-    const int64_t cut = (each + 1) * more;
-    return u < cut ? int(u / (each + 1)) : more + int((u - cut) / each);
+  __device__ __forceinline__ int holder(int u) const {
+    const int cut = (each + 1) * more;
+    return u < cut ? u / (each + 1) : more + (u - cut) / each;
   }
 };
+
+// Where a CTA starts: its tiles [u0, u1), the row that holds u0 and the
+// tiles before that row.
+struct Start {
+  int u0, u1, b, row_at;
+  RowTiles rt;
+};
+
+// A warp's lanes together, one row per lane.
+__device__ __forceinline__ Start find_start(const Rows& r, int C, int c) {
+  const int lane = threadIdx.x & 31;
+  RowTiles mine{};
+  if (lane < r.B) mine = row_tiles(r, lane);
+  int sum = mine.n;
+  for (int b = lane + 32; b < r.B; b += 32) sum += row_tiles(r, b).n;
+  const Shares sh(__reduce_add_sync(0xffffffffu, sum) * r.H, C);
+  Start s;
+  s.u0 = sh.first(c);
+  s.u1 = sh.first(c + 1);
+  s.b = s.row_at = 0;
+  if (s.u0 >= s.u1) return s;
+  int base = 0;
+  for (int b0 = 0;; b0 += 32) {     // some row holds u0
+    if (b0 > 0) {
+      mine.n = 0;
+      if (b0 + lane < r.B) mine = row_tiles(r, b0 + lane);
+    }
+    const int n = mine.n * r.H;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, s.u0 < base + inc);
+    if (hit) {
+      const int f = __ffs(hit) - 1;
+      s.b = b0 + f;
+      s.row_at = base + __shfl_sync(0xffffffffu, inc - n, f);
+      s.rt.start = __shfl_sync(0xffffffffu, mine.start, f);
+      s.rt.len = __shfl_sync(0xffffffffu, mine.len, f);
+      s.rt.t0 = __shfl_sync(0xffffffffu, mine.t0, f);
+      s.rt.n = __shfl_sync(0xffffffffu, mine.n, f);
+      s.rt.pos = __shfl_sync(0xffffffffu, mine.pos, f);
+      return s;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
 
 // Partial result records: m[G], l[G], padding to 16 bytes, acc[G][128].
 __host__ __device__ constexpr int part_acc(int G) { return (2 * G + 3) & ~3; }
@@ -138,6 +164,7 @@ enum : int {
 struct __align__(8) Tile {
   int b, h, blk, flags;
   int lo, hi;     // visible slots of the block (lo >= hi: nothing to read)
+  int pos, pad;   // of the query
 };
 
 template <bool kInt8, int GP>
@@ -318,22 +345,21 @@ __device__ __forceinline__ uint32_t next_term(float& a, float& b) {
 struct Walker {
   Rows rows;
   const int32_t* blocks;
-  int64_t u, u0, u1, row_at;
-  int b;
+  int u, u0, u1, row_at, b;
   RowTiles rt;
   // current (row, head): tiles [j, je) are left
   int h, j, je, seg_flags;
   bool emitted;
 
   __device__ __forceinline__ void open() {   // at tile u < u1
-    while (u >= row_at + int64_t(rt.n) * rows.H) {
-      row_at += int64_t(rt.n) * rows.H;
+    while (u >= row_at + rt.n * rows.H) {
+      row_at += rt.n * rows.H;
       rt = row_tiles(rows, ++b);
     }
-    h = int((u - row_at) / rt.n);
-    const int64_t p0 = row_at + int64_t(h) * rt.n, p1 = p0 + rt.n;
-    j = int(u - p0);
-    je = int(min(u1, p1) - p0);
+    h = (u - row_at) / rt.n;
+    const int p0 = row_at + h * rt.n, p1 = p0 + rt.n;
+    j = u - p0;
+    je = min(u1, p1) - p0;
     seg_flags = (p0 >= u0 && p1 <= u1 ? kWhole : 0) | (p0 < u0 ? 0 : kSlot1);
     emitted = false;
     u += je - j;
@@ -346,6 +372,7 @@ struct Walker {
           emitted = true;
           t.b = b; t.h = h; t.blk = 0; t.lo = t.hi = 0;
           t.flags = seg_flags | kFirst;
+          t.pos = rt.pos;
           return true;
         }
         if (u >= u1) return false;
@@ -367,6 +394,7 @@ struct Walker {
       t.lo = max(0, rt.start - blk * kKv8Block);
       t.hi = min(kKv8Block, rt.len - blk * kKv8Block);
       t.flags = seg_flags | (emitted ? 0 : kFirst);
+      t.pos = rt.pos;
       emitted = true;
       return true;
     }
@@ -427,18 +455,19 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (warp == kLoadWarp) {
     // ------------------------------------------------------ tiles and TMA
     Walker w;
-    w.rows = Rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
+    w.rows = Rows{a.kv_start, a.kv_len, a.q_pos, a.max_pos,
+                  a.B, a.L, a.H, a.K, a.listed};
     w.blocks = a.blocks;
-    const int64_t total = tiles_before(w.rows, a.B) * a.H;
-    const Shares sh(total, gridDim.x);
-    w.u0 = w.u = sh.first(blockIdx.x);
-    w.u1 = sh.first(blockIdx.x + 1);
-    w.b = w.u < w.u1 ? find_row(w.rows, w.u, &w.row_at) : 0;
+    const Start st = find_start(w.rows, gridDim.x, blockIdx.x);
+    w.u0 = w.u = st.u0;
+    w.u1 = st.u1;
+    w.b = st.b;
+    w.row_at = st.row_at;
+    w.rt = st.rt;
     w.j = 0;
     w.je = -1;
     w.emitted = true;
     if (lane == 0) {
-      if (w.u < w.u1) w.rt = row_tiles(w.rows, w.b);
       auto load = [&](const CUtensorMap* map, int full, uint32_t at,
                       const Tile& x) {
         if (x.lo < x.hi) {
@@ -463,7 +492,11 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         more = w.next(nxt);
         if (!more || (nxt.flags & kFirst)) cur.flags |= kLast;
         const int s = i % C::kKStages;
-        if (i >= C::kKStages) ok = wait(C::bKEmpty + s, i / C::kKStages - 1);
+        // the first query's loads go before the flood of all CTAs' first
+        // tiles, in which they took 7 us instead of 1
+        if (i == 1) ok = wait(C::bQ, 0);
+        if (i >= C::kKStages)
+          ok = ok && wait(C::bKEmpty + s, i / C::kKStages - 1);
         if (!ok) break;
         load(&tm_k, C::bKFull + s, sbase + s * kTile, cur);
         ring[i % kDecRing] = cur;
@@ -560,27 +593,37 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int h0 = group * GH, sync_id = 1 + group;
     const uint32_t my_tmem = tmem + (uint32_t(quad * 32) << 16) + h0;
     int seg = -1;
-    // Query of a (row, head): rotated, split into terms, thread t channel t.
-    // Called when the scores of the (row, head) before are all done, so that
-    // the terms may overwrite its own; buf: which of two sets of scales.
-    auto make_q = [&](int b, int h, int buf) {
-      const int pos = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
+    // Query of a (row, head), thread t channel t: its two members of the
+    // rotation and their angle are fetched ahead of the tile that needs
+    // them, ...
+    uint32_t q_raw[GH];
+    float2 q_cs;
+    const bool low = a.half ? t < 64 : (t & 1) == 0;
+    auto fetch_q = [&](const Tile& x) {
       const int k = a.half ? (t & 63) : (t >> 1);
-      const bool low = a.half ? t < 64 : (t & 1) == 0;
-      const int ia = a.half ? k : 2 * k, ib = a.half ? k + 64 : 2 * k + 1;
-      const float2 cs = __ldg(reinterpret_cast<const float2*>(a.table) +
-                              int64_t(pos) * (kHeadDim / 2) + k);
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                               (int64_t(b) * a.H + h) * a.G * kHeadDim;
+      q_cs = __ldg(reinterpret_cast<const float2*>(a.table) +
+                   int64_t(x.pos) * (kHeadDim / 2) + k);
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                          ((int64_t(x.b) * a.H + x.h) * a.G + h0) * kHeadDim;
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        q_raw[g] = 0;
+        if (h0 + g >= a.G) continue;
+        const uint16_t* row = q + g * kHeadDim;
+        q_raw[g] = a.half
+                       ? __ldg(row + k) | (uint32_t(__ldg(row + k + 64)) << 16)
+                       : __ldg(reinterpret_cast<const uint32_t*>(row) + k);
+      }
+    };
+    // ... then rotated and split into terms. Called when the scores of the
+    // (row, head) before are all done, so that the terms may overwrite its
+    // own; buf: which of two sets of scales.
+    auto make_q = [&](int buf) {
       float x[GH];
 #pragma unroll
       for (int g = 0; g < GH; ++g) {
-        x[g] = 0.f;
-        if (h0 + g < a.G) {
-          const float qa = __bfloat162float(q[(h0 + g) * kHeadDim + ia]);
-          const float qb = __bfloat162float(q[(h0 + g) * kHeadDim + ib]);
-          x[g] = low ? qa * cs.x - qb * cs.y : qa * cs.y + qb * cs.x;
-        }
+        const float qa = bf16lo_to_f32(q_raw[g]), qb = bf16hi_to_f32(q_raw[g]);
+        x[g] = low ? qa * q_cs.x - qb * q_cs.y : qa * q_cs.y + qb * q_cs.x;
       }
       float big[GH];
 #pragma unroll
@@ -651,8 +694,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       vs_next = __ldg(a.v_scale + i);
     };
     if (go && !(cur.flags & kEnd)) {
+      fetch_q(cur);
       fetch(cur);
-      make_q(cur.b, cur.h, 0);
+      make_q(0);
       seg = 0;
     }
     // adds the product of tile i, whose weights were scaled by alpha, beta
@@ -685,6 +729,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       const Tile nxt = ring[(i + 1) % kDecRing];
       ks = ks_next;
       vs = vs_next;
+      const bool new_q = !(nxt.flags & kEnd) && (nxt.flags & kFirst);
+      // (two groups of warps leave too few registers to hold it so long)
+      if (C::kGroups == 1 && ok && new_q) fetch_q(nxt);
       if (ok && !(nxt.flags & kEnd)) fetch(nxt);
       if (cur.flags & kFirst) {
         m = -INFINITY;
@@ -788,8 +835,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::bP + (i & 1)));
       // the next (row, head)'s query
-      if (!(nxt.flags & kEnd) && (nxt.flags & kFirst))
-        make_q(nxt.b, nxt.h, (seg + 1) & 1);
+      if (new_q) {
+        if (C::kGroups > 1) fetch_q(nxt);
+        make_q((seg + 1) & 1);
+      }
       // the product of the tile before ran meanwhile
       if (pending) add_o(i - 1, true);
       pending = live;
@@ -855,15 +904,16 @@ __global__ void __launch_bounds__(kJoinThreads)
 kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int64_t where[2];
+  __shared__ int where[2];
   __shared__ float wt[kJoinParts];
   __shared__ float4 part[kJoinGroups][32];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int bh = blockIdx.x / a.G, g = blockIdx.x - bh * a.G;
   const int b = bh / a.H, h = bh - b * a.H;
-  const Rows rows{a.kv_start, a.kv_len, a.B, a.L, a.H, a.K, a.listed};
+  const Rows rows{a.kv_start, a.kv_len, a.q_pos, a.max_pos,
+                  a.B, a.L, a.H, a.K, a.listed};
   if (warp < 2) {
-    const int64_t n = tiles_before(rows, warp == 0 ? a.B : b) * a.H;
+    const int n = tiles_before(rows, warp == 0 ? a.B : b) * a.H;
     if (lane == 0) where[warp] = n;
   }
   const int n = row_tiles(rows, b).n;
@@ -876,7 +926,7 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
   }
   __syncthreads();
   const Shares sh(where[0], C);
-  const int64_t p0 = where[1] + int64_t(h) * n;
+  const int p0 = where[1] + h * n;
   const int c0 = sh.holder(p0), c1 = sh.holder(p0 + n - 1);
   if (c0 == c1) return;       // one CTA held it all
   // CTA c0's part is its second record, those after it have theirs first

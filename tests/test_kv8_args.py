@@ -81,6 +81,7 @@ INV, UNS, WSP = ops.ERR_INVALID_ARG, ops.ERR_UNSUPPORTED, ops.ERR_WORKSPACE
     (decode, {"blocks": None, "K": 1}, INV), (decode, {"Hq": 3}, INV),
     (decode, {"kind": 3}, INV), (decode, {"max_pos": 0}, INV),
     (decode, {"B": -1}, INV), (decode, {"Hq": 34}, UNS),
+    (decode, {"K": 1 << 30, "blocks": P}, UNS),     # tiles in 32 bits
     (decode, {"D": 96}, UNS), (decode, {"dtype": 1}, UNS),
     (decode, {"wsb": 64}, WSP),
     (decode, {"wsb": 64, "blocks": P, "K": 3}, WSP), (decode, {"B": 0, "q": None}, ops.OK),
