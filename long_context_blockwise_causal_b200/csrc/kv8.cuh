@@ -136,19 +136,6 @@ __device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d) {
     return enc2_e4m3(a, b) | (enc2_e4m3(c, d) << 16);
   }
 }
-// Packed products and sums, each rounded once.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-      "mov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  return fma2(b, make_float2(-1.f, -1.f), a);   // the product is exact
-}
 // max that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;

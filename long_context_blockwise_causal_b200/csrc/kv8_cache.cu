@@ -48,6 +48,10 @@ __device__ __forceinline__ uint32_t code2(float x, float y, float inv) {
   return inv > 0.f ? enc2<kInt8>(__fmul_rn(x, inv), __fmul_rn(y, inv)) : 0u;
 }
 
+__device__ __forceinline__ float2 scaled(float2 v, float f) {
+  return make_float2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+}
+
 // Four codes of a block whose scale grew.
 template <bool kInt8>
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
@@ -321,7 +325,7 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
   pdl_trigger();
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
 
-  // loader (thread 0): runs kWrStages - 1 heads ahead over the same items
+  // loader (a lane of the last warp): runs kWrStages - 1 heads ahead over the same items
   int64_t ld_i = blockIdx.x;
   WriteItem ld{};
   int ld_h = 0, ld_n = 0;
@@ -346,7 +350,8 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       ld_seek();
     }
   };
-  if (t == 0) {
+  const bool loader = t == kWrThreads - 32;
+  if (loader) {
     ld_seek();
     for (int s = 0; s < kWrStages - 1; ++s) ld_issue();
   }
@@ -406,9 +411,8 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (it.key) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float2 p = x[k][j], q = y[k][j];
-            x[k][j] = sub2(mul2(p, cc[k][j]), mul2(q, ss[k][j]));
-            y[k][j] = add2(mul2(p, ss[k][j]), mul2(q, cc[k][j]));
+            rotate(x[k][j].x, y[k][j].x, cc[k][j].x, ss[k][j].x);
+            rotate(x[k][j].y, y[k][j].y, cc[k][j].y, ss[k][j].y);
           }
         }
       }
@@ -495,13 +499,13 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       // all have read the tile: its stage is free
       if (!__syncthreads_and(ok)) {
         // a load did not land in time: wait for the others before leaving
-        if (t == 0)
+        if (loader)
           for (int f = n + 1; f < ld_n; ++f)
             mbar_wait(bar(f % kWrStages), (f / kWrStages) & 1, nullptr,
                       status, kWrWaitNs);
         return;
       }
-      if (t == 0) ld_issue();
+      if (loader) ld_issue();
 #pragma unroll
       for (int w = 0; w < kWrWarps; w += 4) {
         const float4 m4 = *reinterpret_cast<const float4*>(red + w);
@@ -512,13 +516,12 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool grew = it.lo > 0 && s > s_old;
       uint8_t* codes = static_cast<uint8_t*>(it.key ? a.codes[0] : a.codes[1]) +
                        (bh * a.L + it.base) * kHeadDim;
-      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
       for (int k = 0; k < kWrPasses; ++k) {
         const int r = row0 + k * kWrStep;
         if (!full && (r < it.lo || r >= it.hi)) continue;
-        const float2 x0 = mul2(x[k][0], inv2), x1 = mul2(x[k][1], inv2);
-        const float2 y0 = mul2(y[k][0], inv2), y1 = mul2(y[k][1], inv2);
+        const float2 x0 = scaled(x[k][0], inv), x1 = scaled(x[k][1], inv);
+        const float2 y0 = scaled(y[k][0], inv), y1 = scaled(y[k][1], inv);
         uint32_t w0, w1;
         if (kHalf) {
           w0 = enc4<kInt8>(x0.x, x0.y, x1.x, x1.y);
@@ -570,35 +573,35 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
           __syncthreads();
         }
       }
-      if (it.key && t < kHeadDim) {
-        const float* chan = reinterpret_cast<const float*>(smem + kWrChan) +
-                            (n & 1) * 2 * kWrWarps * kHeadDim + t;
-        float m0 = INFINITY, m1 = -INFINITY;
+      if (it.key && t < 2 * kHeadDim) {
+        // thread t < 128: lower bound of channel t; then the upper bounds
+        const bool upper = t >= kHeadDim;
+        const int ch = t & (kHeadDim - 1);
+        auto range = [&](int half) {
+          const float* chan =
+              reinterpret_cast<const float*>(smem + kWrChan) +
+              (half * 2 + upper) * kWrWarps * kHeadDim + ch;
+          float v[kWrWarps];
 #pragma unroll
-        for (int w = 0; w < kWrWarps; ++w) {
-          m0 = fminf(m0, chan[w * kHeadDim]);
-          m1 = fmaxf(m1, chan[(kWrWarps + w) * kHeadDim]);
-        }
+          for (int w = 0; w < kWrWarps; ++w) v[w] = chan[w * kHeadDim];
+          float m = v[0];
+#pragma unroll
+          for (int w = 1; w < kWrWarps; ++w)
+            m = upper ? fmaxf(m, v[w]) : fminf(m, v[w]);
+          return m;
+        };
         // encoding keeps the order
-        const float2 f = dec2<kInt8>(code2<kInt8>(m0, m1, inv));
-        float lo = f.x, hi = f.y;
+        const float m = range(n & 1);
+        float code = dec2<kInt8>(code2<kInt8>(m, m, inv)).x;
         if (grew) {
-          const float* old = reinterpret_cast<const float*>(smem + kWrChan) +
-                             ((n & 1) ^ 1) * 2 * kWrWarps * kHeadDim + t;
-#pragma unroll
-          for (int w = 0; w < kWrWarps; ++w) {
-            lo = fminf(lo, old[w * kHeadDim]);
-            hi = fmaxf(hi, old[(kWrWarps + w) * kHeadDim]);
-          }
+          const float old = range((n & 1) ^ 1);
+          code = upper ? fmaxf(code, old) : fminf(code, old);
         }
-        int l = bound_lo<kInt8>(lo), u = bound_hi<kInt8>(hi);
-        int8_t* bd = a.k_bounds + at * 2 * kHeadDim;
-        if (it.lo > 0 && !grew) {   // the older tokens' bounds still hold
-          l = min(l, int(bd[t]));
-          u = max(u, int(bd[kHeadDim + t]));
-        }
-        bd[t] = int8_t(l);
-        bd[kHeadDim + t] = int8_t(u);
+        int bound = upper ? bound_hi<kInt8>(code) : bound_lo<kInt8>(code);
+        int8_t* bd = a.k_bounds + at * 2 * kHeadDim + t;
+        if (it.lo > 0 && !grew)     // the older tokens' bounds still hold
+          bound = upper ? max(bound, int(*bd)) : min(bound, int(*bd));
+        *bd = int8_t(bound);
       }
       if (grew && it.key) __syncthreads();   // the ranges have been read
     }
