@@ -115,7 +115,8 @@ int lwm_kv8_read(const void* k_cache, const void* v_cache,
     return LWM_ERR_INVALID_ARG;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
   if (int64_t(B) * H == 0 || T == 0) return LWM_OK;
-  if (tiles_of(B, T, H) >= (int64_t(1) << 31)) return LWM_ERR_UNSUPPORTED;
+  // a CTA per 32 tokens, head and tensor
+  if (tiles_of(B, T, H) >= (int64_t(1) << 29)) return LWM_ERR_UNSUPPORTED;
   if (!wide_ok({k_rot, v}) || !words_ok({start}) ||
       (L > 0 && !(wide_ok({k_cache, v_cache}) &&
                   words_ok({k_scale, v_scale}))) ||

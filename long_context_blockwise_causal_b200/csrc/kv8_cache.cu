@@ -611,15 +611,13 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
 // ------------------------------------------------------------------ read
 //
 // out[b][t][h] = code * scale of slot start[b] + t, zeros outside
-// [0, min(kv_len[b], L)). A CTA takes 128 tokens of one (row, head) of K or
-// V: eight lanes per row of 128 codes, 16 codes each, four rows per thread
-// with their loads in flight together. Heads are neighbours in the grid,
-// so that a token's heads, adjacent in the output, are written close in
-// time.
+// [0, min(kv_len[b], L)). A CTA takes 32 tokens of one (row, head) of K or
+// V, eight lanes per row of 128 codes, 16 codes each. Heads are neighbours
+// in the grid, so that a token's heads, adjacent in the output, are written
+// close in time. Bound by HBM: 128K tokens x 32 heads in 498 us, the rate of
+// a plain copy; two, four and eight rows per thread took 513, 545 and 557.
 constexpr int kRdThreads = 256;
-constexpr int kRdRows = kRdThreads / 8;
-constexpr int kRdPasses = 4;
-constexpr int kRdTokens = kRdRows * kRdPasses;
+constexpr int kRdTokens = kRdThreads / 8;
 
 template <bool kInt8>
 __global__ void __launch_bounds__(kRdThreads)
@@ -632,47 +630,34 @@ kv8_read_kernel(const __grid_constant__ Kv8ReadArgs a, int tiles) {
   const int h = int(e % uint32_t(a.H));
   e /= uint32_t(a.H);
   const int b = int(e / uint32_t(tiles));
-  const int t0 = int(e - uint32_t(b) * uint32_t(tiles)) * kRdTokens;
-  const int c = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int tok = int(e - uint32_t(b) * uint32_t(tiles)) * kRdTokens +
+                  (threadIdx.x >> 3);
+  const int c = threadIdx.x & 7;
+  if (tok >= a.T) return;
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
   const int64_t bh = int64_t(b) * a.H + h;
-  const int64_t start = __ldg(a.start + b);
+  const int64_t slot = int64_t(__ldg(a.start + b)) + tok;
   const int len = a.kv_len ? min(__ldg(a.kv_len + b), a.L) : a.L;
-  const uint4* codes =
-      static_cast<const uint4*>(key ? a.codes[0] : a.codes[1]) +
-      bh * a.L * 8 + c;
-  const float* scale = (key ? a.scale[0] : a.scale[1]) + bh * nblk;
-  uint4 w[kRdPasses];
-  float s[kRdPasses];
-#pragma unroll
-  for (int i = 0; i < kRdPasses; ++i) {
-    const int tok = t0 + row + i * kRdRows;
-    const int64_t slot = start + tok;
-    w[i] = make_uint4(0, 0, 0, 0);
-    s[i] = 0.f;
-    if (tok < a.T && slot >= 0 && slot < len) {
-      w[i] = __ldg(codes + slot * 8);
-      s[i] = __ldg(scale + slot / kKv8Block);
-    }
+  uint4 w = make_uint4(0, 0, 0, 0);
+  float s = 0.f;
+  if (slot >= 0 && slot < len) {
+    w = __ldg(static_cast<const uint4*>(key ? a.codes[0] : a.codes[1]) +
+              (bh * a.L + slot) * 8 + c);
+    s = __ldg((key ? a.scale[0] : a.scale[1]) + bh * nblk + slot / kKv8Block);
   }
-  uint4* out = static_cast<uint4*>(key ? a.out[0] : a.out[1]) + c * 2;
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < kRdPasses; ++i) {
-    const int tok = t0 + row + i * kRdRows;
-    if (tok >= a.T) continue;
-    const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f0 = dec2<kInt8>(ws[k] & 0xffffu);
-      const float2 f1 = dec2<kInt8>(ws[k] >> 16);
-      o[2 * k] = pack_bf16x2(f0.x * s[i], f0.y * s[i]);
-      o[2 * k + 1] = pack_bf16x2(f1.x * s[i], f1.y * s[i]);
-    }
-    uint4* dst = out + ((int64_t(b) * a.T + tok) * a.H + h) * 16;
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  for (int k = 0; k < 4; ++k) {
+    const float2 f0 = dec2<kInt8>(ws[k] & 0xffffu);
+    const float2 f1 = dec2<kInt8>(ws[k] >> 16);
+    o[2 * k] = pack_bf16x2(f0.x * s, f0.y * s);
+    o[2 * k + 1] = pack_bf16x2(f1.x * s, f1.y * s);
   }
+  uint4* dst = static_cast<uint4*>(key ? a.out[0] : a.out[1]) +
+               ((int64_t(b) * a.T + tok) * a.H + h) * 16 + c * 2;
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <bool kInt8, bool kHalf>

@@ -98,6 +98,7 @@ def check_write(c, kind, layout, T, start, n_new=None, seed=3, scale=1.0):
                   n_new=None if n_new is None else i32(n_new),
                   rope_layout=layout)
     torch.cuda.synchronize()
+    assert ops.last_status() == ops.OK
     after = snap(c)
     q = oracle.KV8_QMAX[kind]
     kb0, kb1 = before[4], after[4]
@@ -168,6 +169,16 @@ def test_write_matches_the_definition(cuda_dev, kind, layout, L, T, start,
                                       n_new):
     c = filled(5, L, 2, kind, seed=1)
     check_write(c, kind, layout, T, start, n_new)
+
+
+@pytest.mark.parametrize("H,T,start", [(5, 4500, [130, 0]), (3, 9000, [61, 0]),
+                                       (1, 14000, [0, 500])])
+@pytest.mark.parametrize("kind,layout", [("e4m3", "half"),
+                                         ("int8", "interleaved")])
+def test_long_writes_match_the_definition(cuda_dev, kind, layout, H, T, start):
+    # several blocks per CTA, runs of one and of several heads
+    c = filled(2, 14600, H, kind, seed=1)
+    check_write(c, kind, layout, T, start, [T, T - 131])
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -65,6 +65,7 @@ INV, UNS, WSP = ops.ERR_INVALID_ARG, ops.ERR_UNSUPPORTED, ops.ERR_WORKSPACE
     (read, {"kc": None}, INV), (read, {"start": OFF}, INV),
     (read, {"kv_len": OFF}, INV), (read, {"T": -4}, INV),
     (read, {"k": None}, INV), (read, {"kind": -1}, INV),
+    (read, {"H": 1 << 18, "T": 1 << 18}, UNS),      # too many CTAs
     (read, {"D": 256}, UNS), (read, {"dtype": 1}, UNS),
     (read, {"T": 0, "k": None}, ops.OK), (read, {"B": 0}, ops.OK),
     (select, {"kb": None}, INV), (select, {"scores": OFF}, INV),
