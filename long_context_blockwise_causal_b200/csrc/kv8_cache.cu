@@ -48,10 +48,6 @@ __device__ __forceinline__ uint32_t code2(float x, float y, float inv) {
   return inv > 0.f ? enc2<kInt8>(__fmul_rn(x, inv), __fmul_rn(y, inv)) : 0u;
 }
 
-__device__ __forceinline__ float2 scaled(float2 v, float f) {
-  return make_float2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
-}
-
 // Four codes of a block whose scale grew.
 template <bool kInt8>
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
@@ -242,65 +238,281 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
 
 // ----------------------------------------------------------- many tokens
 //
-// A CTA takes a block of 128 slots of K or V for a group of heads, one head
-// after the other: the heads' [128 tokens][128] bf16 boxes come in by TMA
-// through a ring of stages, while the rotation's angles of the block's
-// tokens stay in registers. 16 lanes share a token, eight channels each,
-// four tokens per thread; the rotated block stays in registers between the
-// maximum and the encoding, so each input is read once and each code
-// written once. K keeps the channels' smallest and largest value, which
-// give the block's maximum as well as its bounds. One barrier per head.
-constexpr int kWrThreads = 512;
-constexpr int kWrWarps = kWrThreads / 32;
+// A CTA takes a block of 128 slots for a run of heads: K of all of them,
+// then V. The heads' [128 tokens][128] bf16 boxes come in by TMA through a
+// ring of stages, the angles of the block's tokens (512 bytes each, any
+// positions) by one bulk copy per token, while V of the block before is
+// worked on. Two groups of eight warps take the boxes in turn, so that one
+// computes while the other waits. 16 lanes share a token, eight channels
+// each (4c .. 4c + 3 and the same 64 further up), eight tokens per thread;
+// the rotated block stays in registers between the maximum and the
+// encoding, so each input is read once and each code written once. K keeps
+// the channels' smallest and largest value, which give the block's maximum
+// as well as its bounds. One barrier of the group per box.
+constexpr int kWrGroups = 2;
+constexpr int kWrGroup = 256;                       // threads of a group
+constexpr int kWrWarps = kWrGroup / 32;
+constexpr int kWrThreads = kWrGroups * kWrGroup + 32;  // and the loader's
 constexpr int kWrLanes = 16;
-constexpr int kWrStep = kWrThreads / kWrLanes;     // tokens per pass
+constexpr int kWrStep = kWrGroup / kWrLanes;        // tokens per pass
 constexpr int kWrPasses = kKv8Block / kWrStep;
 constexpr int kWrStages = 4;
 constexpr int kWrTile = kKv8Block * kHeadDim * 2;
+constexpr int kWrAngles = kKv8Block * kHeadDim * 4;  // 64 pairs per token
 constexpr uint64_t kWrWaitNs = 4000000000ull;
-// shared memory (bytes): stages, channel ranges [2][lo, hi][warp][128],
-// maxima [2][warp], barriers
-constexpr int kWrChan = kWrStages * kWrTile;
-constexpr int kWrMax = kWrChan + 2 * 2 * kWrWarps * kHeadDim * 4;
-constexpr int kWrBars = kWrMax + 2 * kWrWarps * 4;
-constexpr int kWrSmem = kWrBars + kWrStages * 8 + 128;
-static_assert(kWrSmem <= 232448, "shared memory per CTA");
 
-struct WriteItem {
-  int b, h0, h1;
-  bool key;
-  int64_t base;       // first slot of the block
+// A box and where its codes go.
+struct __align__(16) WriteBox {
+  int64_t codes;      // first code of the block
+  int64_t at;         // its scale
   int lo, hi;         // its new slots
-  int64_t tok;        // token of the block's first slot (may be negative)
-  bool any;
+  int flags;          // kBoxKey, kBoxEnd
+  int item;           // counts the CTA's blocks (angles)
 };
+enum : int { kBoxKey = 1, kBoxEnd = 2 };
+
+// shared memory (bytes): stages, angles, channel ranges
+// [group][box parity][lo, hi][warp][128], maxima [group][parity][warp],
+// boxes, barriers
+constexpr int kWrAng = kWrStages * kWrTile;
+constexpr int kWrChan = kWrAng + kWrAngles;
+constexpr int kWrChanHalf = 2 * kWrWarps * kHeadDim * 4;   // one parity
+constexpr int kWrMax = kWrChan + kWrGroups * 2 * kWrChanHalf;
+constexpr int kWrBox = kWrMax + kWrGroups * 2 * kWrWarps * 4;
+constexpr int kWrBars = kWrBox + kWrStages * int(sizeof(WriteBox));
+constexpr int wFull = 0, wEmpty = kWrStages, wAngles = 2 * kWrStages,
+              kWrNumBars = wAngles + 1;
+constexpr int kWrSmem = kWrBars + kWrNumBars * 8 + 16 + 128;
+static_assert(kWrSmem <= 232448, "shared memory per CTA");
 
 struct WriteGrid {
   int per_row;        // blocks a row's tokens can touch
   int groups, heads;  // head groups and heads in each
-  int64_t items;      // 2 * B * per_row * groups
+  int64_t items;      // B * per_row * groups
 };
 
-__device__ __forceinline__ WriteItem write_item(const Kv8WriteArgs& a,
-                                                const WriteGrid& g,
-                                                int64_t i) {
-  WriteItem w;
-  // all of K, then all of V; within each, heads of a block side by side
-  const int64_t half = g.items / 2;
-  w.key = i < half;
-  if (!w.key) i -= half;
-  const int64_t row_blk = i / g.groups;
-  w.h0 = int(i - row_blk * g.groups) * g.heads;
-  w.h1 = min(w.h0 + g.heads, a.H);
-  w.b = int(row_blk / g.per_row);
-  const NewSlots n = new_slots(a, w.b);
-  w.base = (n.lo / kKv8Block + (row_blk - int64_t(w.b) * g.per_row)) *
-           kKv8Block;
-  w.any = n.lo < n.hi && w.base < n.hi;
-  w.lo = int(max(n.lo - w.base, int64_t(0)));
-  w.hi = int(min(n.hi - w.base, int64_t(kKv8Block)));
-  w.tok = w.base - n.start;
-  return w;
+// Barrier of a group; true if all its threads said so.
+__device__ __forceinline__ bool group_all(int id, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "bar.red.and.pred p, %1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(uint32_t(mine))
+      : "memory");
+  return all != 0;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Where a group finds its box and leaves what its threads exchange: the
+// stage, the group and the parity of its boxes.
+struct WriteWhere {
+  uint8_t* smem;
+  int stage, group, parity;
+  __device__ __forceinline__ float* chan(int parity) const {
+    return reinterpret_cast<float*>(smem + kWrChan +
+                                    (group * 2 + parity) * kWrChanHalf);
+  }
+};
+
+// One box by one group. kFull: every slot of the block is new. False if a
+// warp of the group has given up.
+template <bool kInt8, bool kHalf, bool kKey, bool kFull>
+__device__ __forceinline__ bool write_box(const Kv8WriteArgs& a,
+                                          const WriteBox& box,
+                                          const WriteWhere& w) {
+  const int t = threadIdx.x & (kWrGroup - 1);
+  const int lane = t & 31, wg = t >> 5;
+  const int c = t % kWrLanes, row0 = t / kWrLanes;
+  float* scale = (kKey ? a.scale[0] : a.scale[1]) + box.at;
+  float s_old = 0.f;
+  if (!kFull && box.lo > 0) s_old = __ldcg(scale);
+  // v[k][j]: channel 4c + j of token row0 + 16 k, then 64 + 4c + j - 4
+  float v[kWrPasses][8];
+#pragma unroll
+  for (int k = 0; k < kWrPasses; ++k) {
+    const uint8_t* row =
+        w.smem + w.stage * kWrTile + (row0 + k * kWrStep) * (kHeadDim * 2);
+    const uint2 u = *reinterpret_cast<const uint2*>(row + c * 8);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 128 + c * 8);
+    v[k][0] = bf16lo_to_f32(u.x); v[k][1] = bf16hi_to_f32(u.x);
+    v[k][2] = bf16lo_to_f32(u.y); v[k][3] = bf16hi_to_f32(u.y);
+    v[k][4] = bf16lo_to_f32(x.x); v[k][5] = bf16hi_to_f32(x.x);
+    v[k][6] = bf16lo_to_f32(x.y); v[k][7] = bf16hi_to_f32(x.y);
+    if (kKey) {
+      const float4* ang = reinterpret_cast<const float4*>(
+          w.smem + kWrAng + (row0 + k * kWrStep) * (kHeadDim * 4));
+      if (kHalf) {          // pairs 4c .. 4c + 3
+        const float4 p = ang[2 * c], q = ang[2 * c + 1];
+        rotate(v[k][0], v[k][4], p.x, p.y);
+        rotate(v[k][1], v[k][5], p.z, p.w);
+        rotate(v[k][2], v[k][6], q.x, q.y);
+        rotate(v[k][3], v[k][7], q.z, q.w);
+      } else {              // pairs 2c, 2c + 1 and 32 + 2c, 33 + 2c
+        const float4 p = ang[c], q = ang[16 + c];
+        rotate(v[k][0], v[k][1], p.x, p.y);
+        rotate(v[k][2], v[k][3], p.z, p.w);
+        rotate(v[k][4], v[k][5], q.x, q.y);
+        rotate(v[k][6], v[k][7], q.z, q.w);
+      }
+    }
+  }
+  auto on = [&](int k) {
+    const int r = row0 + k * kWrStep;
+    return r >= box.lo && r < box.hi;
+  };
+  float amax = 0.f;
+  // the warp has read the box and its angles
+  __syncwarp();
+  if (lane == 0)
+    mbar_arrive(smem_u32(w.smem) + kWrBars + 8u * (wEmpty + w.stage));
+  if (kKey) {
+    // lanes 0-15 keep the smallest values of the warp's two tokens of each
+    // pass, the others the largest
+    const bool low = lane < kWrLanes;
+    bool some = kFull;
+    float m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float mn, mx;
+      if (kFull) {
+        mn = min_nan(v[0][j], v[1][j]);
+        mx = max_nan(v[0][j], v[1][j]);
+#pragma unroll
+        for (int k = 2; k < kWrPasses; k += 2) {
+          mn = min3_nan(mn, v[k][j], v[k + 1][j]);
+          mx = max3_nan(mx, v[k][j], v[k + 1][j]);
+        }
+      } else {
+        mn = INFINITY;
+        mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWrPasses; ++k) {
+          if (!on(k)) continue;
+          some = true;
+          mn = min_nan(mn, v[k][j]);
+          mx = max_nan(mx, v[k][j]);
+        }
+      }
+      const float got = __shfl_xor_sync(0xffffffffu, low ? mx : mn, 16);
+      m[j] = low ? min_nan(mn, got) : max_nan(mx, got);
+    }
+    float* to = w.chan(w.parity) + (low ? wg : kWrWarps + wg) * kHeadDim + 4 * c;
+    *reinterpret_cast<float4*>(to) = make_float4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<float4*>(to + 64) =
+        make_float4(m[4], m[5], m[6], m[7]);
+    // a warp none of whose tokens is new has nothing to add
+    if (__any_sync(0xffffffffu, some))
+      amax = max3_abs_nan(max3_abs_nan(m[0], m[1], m[2]),
+                          max3_abs_nan(m[3], m[4], m[5]),
+                          max_nan(fabsf(m[6]), fabsf(m[7])));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kWrPasses; ++k) {
+      if (!kFull && !on(k)) continue;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        amax = max3_abs_nan(amax, v[k][j], v[k][j + 1]);
+    }
+  }
+  amax = warp_max_abs(amax);
+  float* red = reinterpret_cast<float*>(w.smem + kWrMax) +
+               (w.group * 2 + w.parity) * kWrWarps;
+  if (lane == 0) red[wg] = amax;
+  if (!group_all(1 + w.group, true)) return false;
+  {
+    const float4 p = *reinterpret_cast<const float4*>(red);
+    const float4 q = *reinterpret_cast<const float4*>(red + 4);
+    amax = max3_nan(max3_nan(p.x, p.y, p.z), max3_nan(p.w, q.x, q.y),
+                    max_nan(q.z, q.w));
+  }
+  const float sc = block_scale<kInt8>(s_old, amax);
+  const float inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
+  const bool grew = !kFull && box.lo > 0 && sc > s_old;
+  uint8_t* codes =
+      static_cast<uint8_t*>(kKey ? a.codes[0] : a.codes[1]) + box.codes;
+  uint8_t* mine = codes + row0 * kHeadDim + 4 * c;
+#pragma unroll
+  for (int k = 0; k < kWrPasses; ++k) {
+    if (!kFull && !on(k)) continue;
+    uint32_t w0 = enc4<kInt8>(
+        __fmul_rn(v[k][0], inv), __fmul_rn(v[k][1], inv),
+        __fmul_rn(v[k][2], inv), __fmul_rn(v[k][3], inv));
+    uint32_t w1 = enc4<kInt8>(
+        __fmul_rn(v[k][4], inv), __fmul_rn(v[k][5], inv),
+        __fmul_rn(v[k][6], inv), __fmul_rn(v[k][7], inv));
+    if (!(inv > 0.f)) w0 = w1 = 0u;       // whatever the values are
+    *reinterpret_cast<uint32_t*>(mine + k * kWrStep * kHeadDim) = w0;
+    *reinterpret_cast<uint32_t*>(mine + k * kWrStep * kHeadDim + 64) = w1;
+  }
+  if (t == 0) *scale = sc;
+  float* old_chan = w.chan(w.parity ^ 1);
+  if (grew) {
+    // the block's older codes, rounded again: four channels per thread,
+    // their range through the other half of the channel ranges
+    const float ratio = __fdiv_rn(s_old, sc);
+    const int c4 = lane * 4;
+    float lo4[4], hi4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo4[j] = INFINITY;
+      hi4[j] = -INFINITY;
+    }
+    for (int r = wg; r < box.lo; r += kWrWarps) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(codes + r * kHeadDim + c4);
+      const uint32_t u = recode4<kInt8>(*p, ratio);
+      *p = u;
+      const float2 f = dec2<kInt8>(u & 0xffffu), g = dec2<kInt8>(u >> 16);
+      const float x[4] = {f.x, f.y, g.x, g.y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo4[j] = fminf(lo4[j], x[j]);
+        hi4[j] = fmaxf(hi4[j], x[j]);
+      }
+    }
+    *reinterpret_cast<float4*>(old_chan + wg * kHeadDim + c4) =
+        make_float4(lo4[0], lo4[1], lo4[2], lo4[3]);
+    *reinterpret_cast<float4*>(old_chan + (kWrWarps + wg) * kHeadDim + c4) =
+        make_float4(hi4[0], hi4[1], hi4[2], hi4[3]);
+    named_barrier_sync(1 + w.group, kWrGroup);
+  }
+  if (kKey) {
+    // thread t < 128: lower bound of channel t; then the upper bounds
+    const bool upper = t >= kHeadDim;
+    auto range = [&](const float* from) {
+      const float* p = from + (upper ? kWrWarps * kHeadDim : 0) +
+                       (t & (kHeadDim - 1));
+      float m = p[0];
+#pragma unroll
+      for (int i = 1; i < kWrWarps; ++i) {
+        const float x = p[i * kHeadDim];
+        m = upper ? fmaxf(m, x) : fminf(m, x);
+      }
+      return m;
+    };
+    // encoding keeps the order
+    const float m = range(w.chan(w.parity));
+    float code = dec2<kInt8>(code2<kInt8>(m, m, inv)).x;
+    if (grew) {
+      const float old = range(old_chan);
+      code = upper ? fmaxf(code, old) : fminf(code, old);
+    }
+    int bound = upper ? bound_hi<kInt8>(code) : bound_lo<kInt8>(code);
+    int8_t* bd = a.k_bounds + box.at * 2 * kHeadDim + t;
+    if (!kFull && box.lo > 0 && !grew)     // the older tokens' bounds still hold
+      bound = upper ? max(bound, int(*bd)) : min(bound, int(*bd));
+    *bd = int8_t(bound);
+  }
+  if (grew) named_barrier_sync(1 + w.group, kWrGroup);   // ranges are read
+  return true;
 }
 
 template <bool kInt8, bool kHalf>
@@ -308,303 +520,158 @@ __global__ void __launch_bounds__(kWrThreads, 1)
 kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ Kv8WriteArgs a,
-                 const WriteGrid grid, int* status) {
+                 const __grid_constant__ WriteGrid grid, int* status) {
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~uintptr_t(127));
   const uint32_t sbase = smem_u32(smem);
-  auto bar = [&](int s) { return sbase + kWrBars + 8u * s; };
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int c = t % kWrLanes, row0 = t / kWrLanes;
-  if (t == 0) {
-    for (int s = 0; s < kWrStages; ++s) mbar_init(bar(s), 1);
+  WriteBox* boxes = reinterpret_cast<WriteBox*>(smem + kWrBox);
+  volatile int* abort_word =
+      reinterpret_cast<volatile int*>(smem + kWrBars + kWrNumBars * 8);
+  auto bar = [&](int i) { return sbase + kWrBars + 8u * i; };
+  auto wait = [&](int i, int phase) {
+    return mbar_wait(bar(i), phase & 1, abort_word, status, kWrWaitNs);
+  };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWrNumBars; ++i)
+      mbar_init(bar(i), i >= wEmpty && i < wEmpty + kWrStages ? kWrWarps : 1);
     fence_mbar_init();
+    *abort_word = 0;
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
 
-  // loader (a lane of the last warp): runs kWrStages - 1 heads ahead over the same items
-  int64_t ld_i = blockIdx.x;
-  WriteItem ld{};
-  int ld_h = 0, ld_n = 0;
-  auto ld_seek = [&]() {
-    while (ld_i < grid.items) {
-      ld = write_item(a, grid, ld_i);
-      ld_h = ld.h0;
-      if (ld.any) return;
-      ld_i += gridDim.x;
-    }
-  };
-  auto ld_issue = [&]() {
-    if (ld_i >= grid.items) return;
-    const int s = ld_n % kWrStages;
-    mbar_arrive_expect_tx(bar(s), kWrTile);
-    // tokens before the first and behind the last one read as zeros
-    tma_load_4d(sbase + s * kWrTile, ld.key ? &tm_k : &tm_v, bar(s), 0, ld_h,
-                int(ld.tok), ld.b);
-    ++ld_n;
-    if (++ld_h >= ld.h1) {
-      ld_i += gridDim.x;
-      ld_seek();
-    }
-  };
-  const bool loader = t == kWrThreads - 32;
-  if (loader) {
-    ld_seek();
-    for (int s = 0; s < kWrStages - 1; ++s) ld_issue();
-  }
-
-  int n = 0;          // heads done
-  for (int64_t i = blockIdx.x; i < grid.items; i += gridDim.x) {
-    const WriteItem it = write_item(a, grid, i);
-    if (!it.any) continue;
-    const bool full = it.lo == 0 && it.hi == kKv8Block;
-    // angles of the thread's tokens, pairs (4c, 4c + 1), (4c + 2, 4c + 3)
-    float2 cc[kWrPasses][2], ss[kWrPasses][2];
-    if (it.key) {
+  if (warp == kWrGroups * kWrWarps) {
+    // -------------------------------------------------------------- loader
+    int n = 0, item = 0, last_key = -1;
+    bool ok = true;
+    for (int64_t i = blockIdx.x; ok && i < grid.items; i += gridDim.x) {
+      // heads of a block are neighbours
+      const int64_t row_blk = i / grid.groups;
+      const int h0 = int(i - row_blk * grid.groups) * grid.heads;
+      const int h1 = min(h0 + grid.heads, a.H);
+      const int b = int(row_blk / grid.per_row);
+      const NewSlots ns = new_slots(a, b);
+      const int64_t base =
+          (ns.lo / kKv8Block + (row_blk - int64_t(b) * grid.per_row)) *
+          kKv8Block;
+      if (ns.lo >= ns.hi || base >= ns.hi) continue;
+      const int lo = int(max(ns.lo - base, int64_t(0)));
+      const int hi = int(min(ns.hi - base, int64_t(kKv8Block)));
+      const int64_t tok = base - ns.start;   // of the block's first slot
+      // the angles before are free once their last K boxes are read
+      for (int m = max(0, n - kWrStages); ok && m <= last_key; ++m)
+        ok = wait(wEmpty + m % kWrStages, m / kWrStages);
+      if (!ok) break;
+      // consecutive positions are consecutive rows of the table: one copy;
+      // one per token (a quarter of the loader's time) only where they jump
+      int p[kKv8Block / 32];
+      const int32_t* pos = a.positions + int64_t(b) * a.T + tok;
 #pragma unroll
-      for (int k = 0; k < kWrPasses; ++k) {
-        const int r = row0 + k * kWrStep;
-        int p = 0;
-        if (r >= it.lo && r < it.hi)
-          p = max(0, min(__ldg(a.positions + int64_t(it.b) * a.T + it.tok + r),
-                         a.max_pos - 1));
-        const float4* tab = reinterpret_cast<const float4*>(
-            a.table + int64_t(p) * kHeadDim) + 2 * c;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 f = __ldg(tab + j);
-          cc[k][j] = make_float2(f.x, f.z);
-          ss[k][j] = make_float2(f.y, f.w);
-        }
+      for (int k = 0; k < kKv8Block / 32; ++k) {
+        const int r = lane + 32 * k;
+        p[k] = r >= lo && r < hi
+                   ? max(0, min(__ldg(pos + r), a.max_pos - 1))
+                   : -1;
       }
-    }
-    for (int h = it.h0; h < it.h1; ++h, ++n) {
-      const int64_t bh = int64_t(it.b) * a.H + h;
-      const int64_t at = bh * nblk + it.base / kKv8Block;
-      float* scale = (it.key ? a.scale[0] : a.scale[1]) + at;
-      const float s_old = it.lo > 0 ? __ldcg(scale) : 0.f;
-      const bool ok = mbar_wait(bar(n % kWrStages), (n / kWrStages) & 1,
-                                nullptr, status, kWrWaitNs);
-      const uint8_t* tile = smem + (n % kWrStages) * kWrTile;
-      // x, y: first and second members of pairs 4c .. 4c + 3
-      float2 x[kWrPasses][2], y[kWrPasses][2];
+      const int first =
+          max(0, min(__ldg(pos + lo), a.max_pos - 1)) - lo;   // of slot 0
+      bool run = true;
 #pragma unroll
-      for (int k = 0; k < kWrPasses; ++k) {
-        const uint8_t* row = tile + (row0 + k * kWrStep) * (kHeadDim * 2);
-        if (kHalf) {
-          const uint2 u = *reinterpret_cast<const uint2*>(row + c * 8);
-          const uint2 v = *reinterpret_cast<const uint2*>(row + 128 + c * 8);
-          x[k][0] = make_float2(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x));
-          x[k][1] = make_float2(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
-          y[k][0] = make_float2(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x));
-          y[k][1] = make_float2(bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(row + c * 16);
-          x[k][0] = make_float2(bf16lo_to_f32(u.x), bf16lo_to_f32(u.y));
-          y[k][0] = make_float2(bf16hi_to_f32(u.x), bf16hi_to_f32(u.y));
-          x[k][1] = make_float2(bf16lo_to_f32(u.z), bf16lo_to_f32(u.w));
-          y[k][1] = make_float2(bf16hi_to_f32(u.z), bf16hi_to_f32(u.w));
-        }
-        if (it.key) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            rotate(x[k][j].x, y[k][j].x, cc[k][j].x, ss[k][j].x);
-            rotate(x[k][j].y, y[k][j].y, cc[k][j].y, ss[k][j].y);
-          }
-        }
-      }
-      float amax = 0.f;
-      // value j of pass k: x of pairs 4c + j for j < 4, then their y
-      auto val = [&](int k, int j) {
-        const float2 v = j < 4 ? x[k][j / 2] : y[k][(j - 4) / 2];
-        return (j & 1) ? v.y : v.x;
-      };
-      static_assert(kWrPasses == 4, "the maxima below take four values");
-      if (it.key) {
-        float mn[8], mx[8];
-        bool some = false;
-        if (full) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            mn[j] = min_nan(min3_nan(val(0, j), val(1, j), val(2, j)),
-                            val(3, j));
-            mx[j] = max_nan(max3_nan(val(0, j), val(1, j), val(2, j)),
-                            val(3, j));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            mn[j] = INFINITY;
-            mx[j] = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kWrPasses; ++k) {
-              const int r = row0 + k * kWrStep;
-              if (r >= it.lo && r < it.hi) {
-                some = true;
-                mn[j] = min_nan(mn[j], val(k, j));
-                mx[j] = max_nan(mx[j], val(k, j));
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mn[j] = min_nan(mn[j], __shfl_xor_sync(0xffffffffu, mn[j], 16));
-          mx[j] = max_nan(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-        }
-        float* chan = reinterpret_cast<float*>(smem + kWrChan) +
-                      ((n & 1) * 2 * kWrWarps + warp) * kHeadDim;
-        // lanes 0-15 keep the smallest values, the others the largest
-        const bool low = lane < kWrLanes;
-        float m[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = low ? mn[j] : mx[j];
-        if (!low) chan += kWrWarps * kHeadDim;
-        if (kHalf) {    // channels 4c .. and 64 + 4c ..
-          *reinterpret_cast<float4*>(chan + 4 * c) =
-              make_float4(m[0], m[1], m[2], m[3]);
-          *reinterpret_cast<float4*>(chan + 64 + 4 * c) =
-              make_float4(m[4], m[5], m[6], m[7]);
-        } else {        // channels 8c .., pairs side by side
-          *reinterpret_cast<float4*>(chan + 8 * c) =
-              make_float4(m[0], m[4], m[1], m[5]);
-          *reinterpret_cast<float4*>(chan + 8 * c + 4) =
-              make_float4(m[2], m[6], m[3], m[7]);
-        }
-        // a warp none of whose tokens is new has nothing to add
-        if (full || __any_sync(0xffffffffu, some)) {
-          amax = max3_abs_nan(max3_abs_nan(m[0], m[1], m[2]),
-                              max3_abs_nan(m[3], m[4], m[5]),
-                              max_nan(fabsf(m[6]), fabsf(m[7])));
-        }
+      for (int k = 0; k < kKv8Block / 32; ++k)
+        run = run && (p[k] < 0 || p[k] == first + lane + 32 * k);
+      run = __all_sync(0xffffffffu, run);
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar(wAngles), (hi - lo) * (kHeadDim * 4));
+      __syncwarp();
+      if (run) {
+        if (lane == 0)
+          bulk_load(sbase + kWrAng + lo * (kHeadDim * 4),
+                    a.table + int64_t(first + lo) * kHeadDim,
+                    (hi - lo) * (kHeadDim * 4), bar(wAngles));
       } else {
 #pragma unroll
-        for (int k = 0; k < kWrPasses; ++k) {
-          const int r = row0 + k * kWrStep;
-          if (full || (r >= it.lo && r < it.hi)) {
-            amax = max3_abs_nan(amax, x[k][0].x, x[k][0].y);
-            amax = max3_abs_nan(amax, x[k][1].x, x[k][1].y);
-            amax = max3_abs_nan(amax, y[k][0].x, y[k][0].y);
-            amax = max3_abs_nan(amax, y[k][1].x, y[k][1].y);
-          }
-        }
+        for (int k = 0; k < kKv8Block / 32; ++k)
+          if (p[k] >= 0)
+            bulk_load(sbase + kWrAng + (lane + 32 * k) * (kHeadDim * 4),
+                      a.table + int64_t(p[k]) * kHeadDim, kHeadDim * 4,
+                      bar(wAngles));
       }
-      amax = warp_max_abs(amax);
-      float* red = reinterpret_cast<float*>(smem + kWrMax) +
-                   (n & 1) * kWrWarps;
-      if (lane == 0) red[warp] = amax;
-      // all have read the tile: its stage is free
-      if (!__syncthreads_and(ok)) {
-        // a load did not land in time: wait for the others before leaving
-        if (loader)
-          for (int f = n + 1; f < ld_n; ++f)
-            mbar_wait(bar(f % kWrStages), (f / kWrStages) & 1, nullptr,
-                      status, kWrWaitNs);
-        return;
+      for (int u = 0; u < 2 * (h1 - h0); ++u, ++n) {
+        const bool key = u < h1 - h0;
+        const int h = key ? h0 + u : h0 + u - (h1 - h0);
+        const int s = n % kWrStages;
+        if (n >= kWrStages) ok = wait(wEmpty + s, n / kWrStages - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          const int64_t bh = int64_t(b) * a.H + h;
+          WriteBox x;
+          x.codes = (bh * a.L + base) * kHeadDim;
+          x.at = bh * nblk + base / kKv8Block;
+          x.lo = lo;
+          x.hi = hi;
+          x.flags = key ? kBoxKey : 0;
+          x.item = item;
+          boxes[s] = x;
+          mbar_arrive_expect_tx(bar(wFull + s), kWrTile);
+          // tokens before the first and behind the last one read as zeros
+          tma_load_4d(sbase + s * kWrTile, key ? &tm_k : &tm_v,
+                      bar(wFull + s), 0, h, int(tok), b);
+        }
+        __syncwarp();
+        if (key) last_key = n;
       }
-      if (loader) ld_issue();
-#pragma unroll
-      for (int w = 0; w < kWrWarps; w += 4) {
-        const float4 m4 = *reinterpret_cast<const float4*>(red + w);
-        amax = max_nan(amax, max_nan(max_nan(m4.x, m4.y), max_nan(m4.z, m4.w)));
-      }
-      const float s = block_scale<kInt8>(s_old, amax);
-      const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-      const bool grew = it.lo > 0 && s > s_old;
-      uint8_t* codes = static_cast<uint8_t*>(it.key ? a.codes[0] : a.codes[1]) +
-                       (bh * a.L + it.base) * kHeadDim;
-#pragma unroll
-      for (int k = 0; k < kWrPasses; ++k) {
-        const int r = row0 + k * kWrStep;
-        if (!full && (r < it.lo || r >= it.hi)) continue;
-        const float2 x0 = scaled(x[k][0], inv), x1 = scaled(x[k][1], inv);
-        const float2 y0 = scaled(y[k][0], inv), y1 = scaled(y[k][1], inv);
-        uint32_t w0, w1;
-        if (kHalf) {
-          w0 = enc4<kInt8>(x0.x, x0.y, x1.x, x1.y);
-          w1 = enc4<kInt8>(y0.x, y0.y, y1.x, y1.y);
-        } else {
-          w0 = enc4<kInt8>(x0.x, y0.x, x0.y, y0.y);
-          w1 = enc4<kInt8>(x1.x, y1.x, x1.y, y1.y);
-        }
-        if (!(inv > 0.f)) w0 = w1 = 0u;     // whatever the values are
-        uint8_t* row = codes + r * kHeadDim;
-        if (kHalf) {
-          *reinterpret_cast<uint32_t*>(row + c * 4) = w0;
-          *reinterpret_cast<uint32_t*>(row + 64 + c * 4) = w1;
-        } else {
-          *reinterpret_cast<uint2*>(row + c * 8) = make_uint2(w0, w1);
-        }
-      }
-      if (t == 0) *scale = s;
-      if (grew) {
-        // the block's older codes, rounded again: four channels per thread
-        const float ratio = __fdiv_rn(s_old, s);
-        const int c4 = (t & 31) * 4;
-        float lo4[4], hi4[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo4[j] = INFINITY;
-          hi4[j] = -INFINITY;
-        }
-        for (int r = warp; r < it.lo; r += kWrWarps) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(codes + r * kHeadDim + c4);
-          const uint32_t w = recode4<kInt8>(*p, ratio);
-          *p = w;
-          const float2 f = dec2<kInt8>(w & 0xffffu), g = dec2<kInt8>(w >> 16);
-          const float v[4] = {f.x, f.y, g.x, g.y};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            lo4[j] = fminf(lo4[j], v[j]);
-            hi4[j] = fmaxf(hi4[j], v[j]);
-          }
-        }
-        if (it.key) {
-          // through the other half of the channel ranges
-          float* chan = reinterpret_cast<float*>(smem + kWrChan) +
-                        (((n & 1) ^ 1) * 2 * kWrWarps + warp) * kHeadDim + c4;
-          *reinterpret_cast<float4*>(chan) =
-              make_float4(lo4[0], lo4[1], lo4[2], lo4[3]);
-          *reinterpret_cast<float4*>(chan + kWrWarps * kHeadDim) =
-              make_float4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          __syncthreads();
-        }
-      }
-      if (it.key && t < 2 * kHeadDim) {
-        // thread t < 128: lower bound of channel t; then the upper bounds
-        const bool upper = t >= kHeadDim;
-        const int ch = t & (kHeadDim - 1);
-        auto range = [&](int half) {
-          const float* chan =
-              reinterpret_cast<const float*>(smem + kWrChan) +
-              (half * 2 + upper) * kWrWarps * kHeadDim + ch;
-          float v[kWrWarps];
-#pragma unroll
-          for (int w = 0; w < kWrWarps; ++w) v[w] = chan[w * kHeadDim];
-          float m = v[0];
-#pragma unroll
-          for (int w = 1; w < kWrWarps; ++w)
-            m = upper ? fmaxf(m, v[w]) : fminf(m, v[w]);
-          return m;
-        };
-        // encoding keeps the order
-        const float m = range(n & 1);
-        float code = dec2<kInt8>(code2<kInt8>(m, m, inv)).x;
-        if (grew) {
-          const float old = range((n & 1) ^ 1);
-          code = upper ? fmaxf(code, old) : fminf(code, old);
-        }
-        int bound = upper ? bound_hi<kInt8>(code) : bound_lo<kInt8>(code);
-        int8_t* bd = a.k_bounds + at * 2 * kHeadDim + t;
-        if (it.lo > 0 && !grew)     // the older tokens' bounds still hold
-          bound = upper ? max(bound, int(*bd)) : min(bound, int(*bd));
-        *bd = int8_t(bound);
-      }
-      if (grew && it.key) __syncthreads();   // the ranges have been read
+      ++item;
     }
+    // one end for each group, behind all boxes
+    const int loads = n;
+    for (int g = 0; ok && g < kWrGroups; ++g, ++n) {
+      const int s = n % kWrStages;
+      if (n >= kWrStages) ok = wait(wEmpty + s, n / kWrStages - 1);
+      if (ok && lane == 0) {
+        boxes[s].flags = kBoxEnd;
+        mbar_arrive(bar(wFull + s));
+      }
+      __syncwarp();
+    }
+    // no load is in flight when the CTA leaves, abandoned or not (a stage
+    // that an end has taken was empty before)
+    for (int m = max(0, n - kWrStages); m < loads; ++m)
+      mbar_wait(bar(wFull + m % kWrStages), (m / kWrStages) & 1, nullptr,
+                status, kWrWaitNs);
+    if (item > 0)
+      mbar_wait(bar(wAngles), (item - 1) & 1, nullptr, status, kWrWaitNs);
+    return;
+  }
+
+  // ---------------------------------------------------------------- groups
+  const int group = warp / kWrWarps;
+  for (int n = group, parity = 0;; n += kWrGroups, parity ^= 1) {
+    const int s = n % kWrStages;
+    // the end and a wait that gave up are agreed on, warp by warp here and by
+    // the whole group at the box's barrier, so that no thread is left alone
+    bool ok = __all_sync(0xffffffffu, wait(wFull + s, n / kWrStages));
+    const WriteBox box = boxes[s];
+    if (ok) ok = !(box.flags & kBoxEnd);
+    if (ok && (box.flags & kBoxKey))
+      ok = __all_sync(0xffffffffu, wait(wAngles, box.item));
+    if (!ok) {
+      group_all(1 + group, false);
+      break;
+    }
+    const bool key = box.flags & kBoxKey;
+    const bool full = box.lo == 0 && box.hi == kKv8Block;
+    const WriteWhere w{smem, s, group, parity};
+    if (key)
+      ok = full ? write_box<kInt8, kHalf, true, true>(a, box, w)
+                : write_box<kInt8, kHalf, true, false>(a, box, w);
+    else
+      ok = full ? write_box<kInt8, kHalf, false, true>(a, box, w)
+                : write_box<kInt8, kHalf, false, false>(a, box, w);
+    if (!ok) break;
   }
 }
 
@@ -678,13 +745,14 @@ cudaError_t launch_many(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
   const int sms = sm_count();
   WriteGrid g{};
   g.per_row = (a.T + kKv8Block - 1) / kKv8Block + 1;
-  // as many heads per item as leave each SM four items or more: a longer
-  // run reuses the angles, a shorter one spreads the work
-  const int64_t tiles = 2 * int64_t(a.B) * g.per_row * a.H;
-  g.heads = int(std::max<int64_t>(
-      1, std::min<int64_t>({16, tiles / (4 * sms), a.H})));
-  g.groups = (a.H + g.heads - 1) / g.heads;
-  g.items = 2 * int64_t(a.B) * g.per_row * g.groups;
+  // as many heads per item as leave each SM six items or more: a longer run
+  // reuses the angles, a shorter one spreads the work
+  const int64_t heads = int64_t(a.B) * g.per_row * a.H;
+  const int most = int(std::max<int64_t>(
+      1, std::min<int64_t>({16, heads / (6 * sms), a.H})));
+  g.groups = (a.H + most - 1) / most;
+  g.heads = (a.H + g.groups - 1) / g.groups;
+  g.items = int64_t(a.B) * g.per_row * g.groups;
   const cudaError_t e = allow_smem<kv8_write_kernel<kInt8, kHalf>>(kWrSmem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = std::min<int64_t>(g.items, sms);
