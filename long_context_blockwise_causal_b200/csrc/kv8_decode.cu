@@ -937,6 +937,18 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = c0; c <= c1; c += kJoinParts) {
     const int k = min(kJoinParts, c1 + 1 - c);
+    // the accumulators come in while their weights are worked out
+    constexpr int kMine = kJoinParts / kJoinGroups;
+    float4 x[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int j = warp + i * kJoinGroups;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < k)
+        x[i] = __ldcg(reinterpret_cast<const float4*>(
+                          record(c + j) + part_acc(a.G) + g * kHeadDim) +
+                      lane);
+    }
     // every warp forms the pass's maximum and sum (lane: parts lane, + 32)
     float mp[2], lp[2];
     float mx = m;
@@ -964,14 +976,15 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
     m = mx;
     acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
     __syncthreads();
-    for (int j = warp; j < k; j += kJoinGroups) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int j = warp + i * kJoinGroups;
+      if (j >= k) break;
       const float w = wt[j];
-      const float4 x = reinterpret_cast<const float4*>(
-          record(c + j) + part_acc(a.G) + g * kHeadDim)[lane];
-      acc.x = fmaf(x.x, w, acc.x);
-      acc.y = fmaf(x.y, w, acc.y);
-      acc.z = fmaf(x.z, w, acc.z);
-      acc.w = fmaf(x.w, w, acc.w);
+      acc.x = fmaf(x[i].x, w, acc.x);
+      acc.y = fmaf(x[i].y, w, acc.y);
+      acc.z = fmaf(x[i].z, w, acc.z);
+      acc.w = fmaf(x[i].w, w, acc.w);
     }
     __syncthreads();
   }

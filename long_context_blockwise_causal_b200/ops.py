@@ -653,79 +653,92 @@ def _kv8_sizes(where, cache):
     code = _KV8_TYPES.get(k.dtype)
     if code is None:
         raise LwmError(ERR_INVALID_ARG, f"{where}: cache.k is {k.dtype}")
-    _expect_dims(where, "cache.k", k, 4)
-    B, H, L, D = k.shape
+    shape = k.shape
+    if len(shape) != 4:
+        _expect_dims(where, "cache.k", k, 4)
+    B, H, L, D = shape
     return B, H, L, D, code
 
 
-def _kv8_group(where, q, B, H, D):
+def _kv8_group(where, q, H):
     """Query heads of q [B,Hq,D], a multiple of the cache's H heads."""
-    _expect_dims(where, "q", q, 3)
-    Hq = q.shape[1]
+    shape = q.shape
+    if len(shape) != 3:
+        _expect_dims(where, "q", q, 3)
+    Hq = shape[1]
     if H and Hq % H:
         raise LwmError(ERR_INVALID_ARG,
                        f"{where}: {Hq} query heads over {H} cache heads")
     return Hq
 
 
-def _kv8_ready(where, cache, B, H, L, D, table, named):
+def _kv8_ready(where, cache, sizes, table, words, wide):
     """Shapes, types and placement of every tensor of a call, before any
-    pointer reaches the library: the cache's, table's and the (name, tensor
-    or None, shape, dtype) of `named`. One pass, as these calls are short."""
+    pointer reaches the library: the cache's, the table's, the int32 vectors
+    in `words` (name, tensor or None) of one entry per row, and those of
+    `wide` (name, tensor or None, shape, dtype). Returns the device. These
+    calls are short, so the usual case is one pass that finds nothing."""
+    B, H, L, D = sizes
     k, v, ks, vs, kb = cache
+    f32, i32 = torch.float32, torch.int32
     n = (L + BLOCK - 1) // BLOCK
-    scales = (B, H, n)
+    scales, rows = (B, H, n), (B,)
     bad = (v.shape != k.shape or v.dtype is not k.dtype
-           or ks.shape != scales or ks.dtype is not torch.float32
-           or vs.shape != scales or vs.dtype is not torch.float32
+           or ks.shape != scales or ks.dtype is not f32
+           or vs.shape != scales or vs.dtype is not f32
            or kb.shape != (B, H, n, 2, D) or kb.dtype is not torch.int8)
-    if table is not None:
-        tshape = table.shape
-        bad = bad or (len(tshape) != 3 or tshape[1:] != (D // 2, 2)
-                      or table.dtype is not torch.float32)
     dev = k.get_device()
-    placed = [k, v, ks, vs, kb]
+    away = (dev < 0 or v.get_device() != dev or ks.get_device() != dev
+            or vs.get_device() != dev or kb.get_device() != dev)
+    loose = not (k.is_contiguous() and v.is_contiguous()
+                 and ks.is_contiguous() and vs.is_contiguous()
+                 and kb.is_contiguous())
     if table is not None:
-        placed.append(table)
-    for _, t, shape, dtype in named:
+        bad |= table.shape[1:] != (D // 2, 2) or table.dtype is not f32
+        away |= table.get_device() != dev
+        loose |= not table.is_contiguous()
+    for _, t in words:
         if t is not None:
-            bad = bad or t.shape != shape or t.dtype is not dtype
-            placed.append(t)
-    if bad:
+            bad |= t.shape != rows or t.dtype is not i32
+            away |= t.get_device() != dev
+            loose |= not t.is_contiguous()
+    for _, t, shape, dtype in wide:
+        if t is not None:
+            bad |= t.shape != shape or t.dtype is not dtype
+            away |= t.get_device() != dev
+            loose |= not t.is_contiguous()
+    if bad or away or loose:
         _expect(where, "cache.v", v, k.shape, k.dtype)
-        _expect(where, "cache.k_scale", ks, scales, torch.float32)
-        _expect(where, "cache.v_scale", vs, scales, torch.float32)
+        _expect(where, "cache.k_scale", ks, scales, f32)
+        _expect(where, "cache.v_scale", vs, scales, f32)
         _expect(where, "cache.k_bounds", kb, (B, H, n, 2, D), torch.int8)
         if table is not None:
             _expect_dims(where, "table", table, 3)
-            _expect(where, "table", table, (table.shape[0], D // 2, 2),
-                    torch.float32)
-        for name, t, shape, dtype in named:
+            _expect(where, "table", table, (table.shape[0], D // 2, 2), f32)
+        for name, t in words:
+            _expect(where, name, t, rows, i32)
+        for name, t, shape, dtype in wide:
             _expect(where, name, t, shape, dtype)
-    for t in placed:
-        if t.get_device() != dev:
-            _same_device(where, *placed)
-        if dev < 0 or not t.is_contiguous():
-            _need_cuda(*placed)
+        every = (k, v, ks, vs, kb, table, *(t for _, t in words),
+                 *(t for _, t, _, _ in wide))
+        _same_device(where, *every)
+        _need_cuda(*every)
     return dev
 
 
-def _kv8_call(fn, dev, stream, *args):
-    """fn(*args, stream) with the tensors' device current; the stream is by
-    default that device's current one."""
-    if stream is None:
-        # the current stream's handle, without building a Stream object
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        handle = stream.cuda_stream
-    call = getattr(lib(), fn)
+def _kv8_call(name, call, dev, stream, args):
+    """call(*args, stream) with the tensors' device current; the stream is
+    by default that device's current one."""
+    # (the current stream's handle, without building a Stream object)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None \
+        else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev:
         st = call(*args, handle)
     else:
         with torch.cuda.device(dev):
             st = call(*args, handle)
     if st != OK:
-        raise LwmError(st, fn)
+        raise LwmError(st, name)
 
 
 def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
@@ -738,18 +751,18 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
     _expect_dims(w, "k", k, 4)
     T = k.shape[1]
     new = (B, T, H, D)
-    dev = _kv8_ready(w, cache, B, H, L, D, table, (
-        ("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
-        ("positions", positions, (B, T), torch.int32),
-        ("start", start, (B,), torch.int32),
-        ("n_new", n_new, (B,), torch.int32)))
-    _kv8_call("lwm_kv8_write", dev, stream, k.data_ptr(), v.data_ptr(),
-              positions.data_ptr(), start.data_ptr(),
-              None if n_new is None else n_new.data_ptr(), table.data_ptr(),
-              table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
-              _layout_code(rope_layout), cache.k.data_ptr(),
-              cache.v.data_ptr(), cache.k_scale.data_ptr(),
-              cache.v_scale.data_ptr(), cache.k_bounds.data_ptr())
+    dev = _kv8_ready(
+        w, cache, (B, H, L, D), table,
+        (("start", start), ("n_new", n_new)),
+        (("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
+         ("positions", positions, (B, T), torch.int32)))
+    _kv8_call("lwm_kv8_write", lib().lwm_kv8_write, dev, stream, (
+        k.data_ptr(), v.data_ptr(), positions.data_ptr(), start.data_ptr(),
+        None if n_new is None else n_new.data_ptr(), table.data_ptr(),
+        table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
+        _layout_code(rope_layout), cache.k.data_ptr(), cache.v.data_ptr(),
+        cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+        cache.k_bounds.data_ptr()))
     return cache
 
 
@@ -763,20 +776,19 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     if T < 0:
         raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
     shape = (B, T, H, D)
-    dev = _kv8_ready(w, cache, B, H, L, D, None, (
-        ("start", start, (B,), torch.int32),
-        ("kv_len", kv_len, (B,), torch.int32),
-        ("k_rot", k_rot, shape, torch.bfloat16),
-        ("v", v, shape, torch.bfloat16)))
+    dev = _kv8_ready(w, cache, (B, H, L, D), None,
+                     (("start", start), ("kv_len", kv_len)),
+                     (("k_rot", k_rot, shape, torch.bfloat16),
+                      ("v", v, shape, torch.bfloat16)))
     if k_rot is None:
         k_rot = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
     if v is None:
         v = torch.empty_like(k_rot)
-    _kv8_call("lwm_kv8_read", dev, stream, cache.k.data_ptr(),
-              cache.v.data_ptr(), cache.k_scale.data_ptr(),
-              cache.v_scale.data_ptr(), start.data_ptr(),
-              None if kv_len is None else kv_len.data_ptr(), B, T, L, H, D,
-              DTYPE_BF16, code, k_rot.data_ptr(), v.data_ptr())
+    _kv8_call("lwm_kv8_read", lib().lwm_kv8_read, dev, stream, (
+        cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+        cache.v_scale.data_ptr(), start.data_ptr(),
+        None if kv_len is None else kv_len.data_ptr(), B, T, L, H, D,
+        DTYPE_BF16, code, k_rot.data_ptr(), v.data_ptr()))
     return k_rot, v
 
 
@@ -789,27 +801,27 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
     w = "kv8_select"
     B, H, L, D, _ = _kv8_sizes(w, cache)
-    Hq = _kv8_group(w, q, B, H, D)
+    Hq = _kv8_group(w, q, H)
     K = int(n_select)
     if K < 1:
         raise LwmError(ERR_INVALID_ARG, f"{w}: n_select is {K}")
-    dev = _kv8_ready(w, cache, B, H, L, D, table, (
-        ("q", q, (B, Hq, D), torch.bfloat16),
-        ("kv_start", kv_start, (B,), torch.int32),
-        ("kv_len", kv_len, (B,), torch.int32),
-        ("q_pos", q_pos, (B,), torch.int32),
-        ("blocks", blocks, (B, H, K), torch.int32),
-        ("scores", scores, (B, H, K), torch.float32)))
+    lists = (B, H, K)
+    dev = _kv8_ready(
+        w, cache, (B, H, L, D), table,
+        (("kv_start", kv_start), ("kv_len", kv_len), ("q_pos", q_pos)),
+        (("q", q, (B, Hq, D), torch.bfloat16),
+         ("blocks", blocks, lists, torch.int32),
+         ("scores", scores, lists, torch.float32)))
     if blocks is None:
-        blocks = torch.empty((B, H, K), dtype=torch.int32, device=q.device)
+        blocks = kv_len.new_empty(lists)
     if scores is None:
-        scores = torch.empty_like(blocks, dtype=torch.float32)
-    _kv8_call("lwm_kv8_select", dev, stream, q.data_ptr(),
-              cache.k_bounds.data_ptr(), cache.k_scale.data_ptr(),
-              kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
-              table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
-              _layout_code(rope_layout), K, int(n_sink), int(n_recent),
-              blocks.data_ptr(), scores.data_ptr())
+        scores = cache.k_scale.new_empty(lists)
+    _kv8_call("lwm_kv8_select", lib().lwm_kv8_select, dev, stream, (
+        q.data_ptr(), cache.k_bounds.data_ptr(), cache.k_scale.data_ptr(),
+        kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
+        table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
+        _layout_code(rope_layout), K, int(n_sink), int(n_recent),
+        blocks.data_ptr(), scores.data_ptr()))
     return blocks, scores
 
 
@@ -827,36 +839,39 @@ def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
     cache head i // (Hq // H). Returns (out [B,Hq,D], lse [B,Hq])."""
     w = "kv8_decode"
     B, H, L, D, code = _kv8_sizes(w, cache)
-    Hq = _kv8_group(w, q, B, H, D)
+    Hq = _kv8_group(w, q, H)
     K = -1
     if blocks is not None:
         _expect_dims(w, "blocks", blocks, 3)
         K = blocks.shape[2]
-    dev = _kv8_ready(w, cache, B, H, L, D, table, (
-        ("q", q, (B, Hq, D), torch.bfloat16),
-        ("kv_start", kv_start, (B,), torch.int32),
-        ("kv_len", kv_len, (B,), torch.int32),
-        ("q_pos", q_pos, (B,), torch.int32),
-        ("blocks", blocks, (B, H, K), torch.int32),
-        ("out", out, (B, Hq, D), torch.bfloat16),
-        ("lse", lse, (B, Hq), torch.float32),
-        ("workspace", workspace, getattr(workspace, "shape", None),
-         getattr(workspace, "dtype", None))))
+    dev = _kv8_ready(
+        w, cache, (B, H, L, D), table,
+        (("kv_start", kv_start), ("kv_len", kv_len), ("q_pos", q_pos)),
+        (("q", q, (B, Hq, D), torch.bfloat16),
+         ("blocks", blocks, (B, H, K), torch.int32),
+         ("out", out, (B, Hq, D), torch.bfloat16),
+         ("lse", lse, (B, Hq), torch.float32),
+         ("workspace", workspace, getattr(workspace, "shape", None),
+          getattr(workspace, "dtype", None))))
+    C = lib()
+    need = C.lwm_kv8_decode_workspace_size(B, L, Hq, H, D, K)
+    if workspace is None:
+        workspace = cache.k_bounds.new_empty(max(need, 1))     # int8: bytes
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise LwmError(ERR_WORKSPACE, "workspace")
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    ws = _workspace(
-        lib().lwm_kv8_decode_workspace_size(B, L, Hq, H, D, K), q.device,
-        workspace)
-    _kv8_call("lwm_kv8_decode", dev, stream, q.data_ptr(),
-              cache.k.data_ptr(), cache.v.data_ptr(),
-              cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-              kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
-              None if blocks is None else blocks.data_ptr(), K,
-              table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
-              code, _layout_code(rope_layout), out.data_ptr(),
-              lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+        lse = cache.k_scale.new_empty((B, Hq))
+    _kv8_call("lwm_kv8_decode", C.lwm_kv8_decode, dev, stream, (
+        q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
+        cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+        kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
+        None if blocks is None else blocks.data_ptr(), K, table.data_ptr(),
+        table.shape[0], B, L, Hq, H, D, DTYPE_BF16, code,
+        _layout_code(rope_layout), out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), have))
     return out, lse
 
 
