@@ -1004,6 +1004,72 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
     a.lse[blockIdx.x] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The same where there are more (row, cache head) pairs than CTAs in the
+// decode kernel, so that most are whole and the others have few parts: one
+// CTA per cut between two shares, a warp per query head. Cut c lies before
+// tile first(c); the pair it runs through is joined at its first cut.
+__global__ void __launch_bounds__(kJoinThreads)
+kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ Start at;
+  __shared__ int tiles;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const Rows rows{a.kv_start, a.kv_len, a.q_pos, a.max_pos,
+                  a.B, a.L, a.H, a.K, a.listed};
+  if (warp == 0) {
+    const Start s = find_start(rows, C, blockIdx.x + 1);
+    if (lane == 0) at = s;
+  } else if (warp == 1) {
+    const int n = tiles_before(rows, a.B) * a.H;
+    if (lane == 0) tiles = n;
+  }
+  // rows that see nothing
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (row_tiles(rows, b).n > 0) continue;
+    const int64_t q0 = int64_t(b) * a.H * a.G;
+    for (int i = t; i < a.H * a.G * (kHeadDim / 2); i += kJoinThreads)
+      reinterpret_cast<uint32_t*>(a.out)[q0 * (kHeadDim / 2) + i] = 0u;
+    for (int i = t; i < a.H * a.G; i += kJoinThreads)
+      a.lse[q0 + i] = -INFINITY;
+  }
+  __syncthreads();
+  if (at.u0 >= at.u1) return;            // no tiles behind the cut
+  const Shares sh(tiles, C);
+  const int h = (at.u0 - at.row_at) / at.rt.n;
+  const int p0 = at.row_at + h * at.rt.n;
+  const int c0 = sh.holder(p0), c1 = sh.holder(p0 + at.rt.n - 1);
+  if (c0 != int(blockIdx.x)) return;     // starts at the cut, or cut before
+  const int64_t q0 = (int64_t(at.b) * a.H + h) * a.G;
+  for (int g = warp; g < a.G; g += kJoinThreads / 32) {
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      const float* rec =
+          a.part + (int64_t(c) * 2 + (c == c0)) * part_stride(a.G);
+      const float mp = __ldcg(rec + g), lp = __ldcg(rec + a.G + g);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(
+                                  rec + part_acc(a.G) + g * kHeadDim) + lane);
+      const float mx = fmaxf(m, mp);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      const float old = exp2f(m - mu), w = exp2f(mp - mu);
+      m = mx;
+      l = l * old + lp * w;
+      acc.x = acc.x * old + x.x * w;
+      acc.y = acc.y * old + x.y * w;
+      acc.z = acc.z * old + x.z * w;
+      acc.w = acc.w * old + x.w * w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                             (q0 + g) * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                   pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0)
+      a.lse[q0 + g] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
 }  // namespace
 
 int kv8_decode_grid(int B, int L, int H, int G, int K) {
@@ -1055,8 +1121,12 @@ cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
       a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;
   note_launch();
-  e = launch_dependent(kv8_combine_kernel, dim3(a.B * a.H * a.G),
-                       dim3(kJoinThreads), 0, st, a, C);
+  // more pairs than CTAs: at the cuts (C > 1: a pair per CTA would else do)
+  e = int64_t(a.B) * a.H > C && C > 1
+          ? launch_dependent(kv8_combine_cuts_kernel, dim3(C - 1),
+                             dim3(kJoinThreads), 0, st, a, C)
+          : launch_dependent(kv8_combine_kernel, dim3(a.B * a.H * a.G),
+                             dim3(kJoinThreads), 0, st, a, C);
   if (e != cudaSuccess) return e;
   note_launch();
   return cudaGetLastError();
