@@ -48,7 +48,7 @@ int query_status(int Hq, int H, int max_pos, int rope_layout) {
   if (Hq < 0 || max_pos < 0 ||
       (rope_layout != LWM_ROPE_INTERLEAVED && rope_layout != LWM_ROPE_HALF))
     return LWM_ERR_INVALID_ARG;
-  if (H > 0 && Hq % H != 0) return LWM_ERR_INVALID_ARG;
+  if (H == 0 ? Hq > 0 : Hq % H != 0) return LWM_ERR_INVALID_ARG;
   if (H > 0 && Hq / H > kKv8MaxGroup) return LWM_ERR_UNSUPPORTED;
   return LWM_OK;
 }

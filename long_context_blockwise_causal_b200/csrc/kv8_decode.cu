@@ -1034,7 +1034,8 @@ kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
       a.lse[q0 + i] = -INFINITY;
   }
   __syncthreads();
-  if (at.u0 >= at.u1) return;            // no tiles behind the cut
+  // a call of one CTA has no cut; and there may be no tiles behind one
+  if (int(blockIdx.x) + 1 >= C || at.u0 >= at.u1) return;
   const Shares sh(tiles, C);
   const int h = (at.u0 - at.row_at) / at.rt.n;
   const int p0 = at.row_at + h * at.rt.n;
@@ -1121,10 +1122,10 @@ cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
       a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;
   note_launch();
-  // more pairs than CTAs: at the cuts (C > 1: a pair per CTA would else do)
-  e = int64_t(a.B) * a.H > C && C > 1
-          ? launch_dependent(kv8_combine_cuts_kernel, dim3(C - 1),
-                             dim3(kJoinThreads), 0, st, a, C)
+  e = int64_t(a.B) * a.H > C
+          ? launch_dependent(kv8_combine_cuts_kernel,
+                             dim3(std::max(C - 1, 1)), dim3(kJoinThreads), 0,
+                             st, a, C)
           : launch_dependent(kv8_combine_kernel, dim3(a.B * a.H * a.G),
                              dim3(kJoinThreads), 0, st, a, C);
   if (e != cudaSuccess) return e;

@@ -10,6 +10,7 @@ tensor that is not on a CUDA device) it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -726,12 +727,11 @@ def _kv8_ready(where, cache, sizes, table, words, wide):
     return dev
 
 
-def _kv8_call(name, call, dev, stream, args):
-    """call(*args, stream) with the tensors' device current; the stream is
-    by default that device's current one."""
+def _kv8_call(name, call, dev, args):
+    """call(*args, stream) with the tensors' device current, on that device's
+    current stream."""
     # (the current stream's handle, without building a Stream object)
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None \
-        else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(dev)
     if torch._C._cuda_getDevice() == dev:
         st = call(*args, handle)
     else:
@@ -741,7 +741,20 @@ def _kv8_call(name, call, dev, stream, args):
         raise LwmError(st, name)
 
 
-def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
+def _on_stream(f):
+    """``stream=``: the call with that stream current, so that what it
+    allocates (results, workspace) belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+@_on_stream
+def kv8_write(cache, k, v, positions, start, table, n_new=None,
               rope_layout="interleaved"):
     """Rotate and quantise k, v [B,T,H,D] bf16 into the cache at slots
     start[b] + t (in place; see the header for the block scales). ``n_new``
@@ -756,7 +769,7 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
         (("start", start), ("n_new", n_new)),
         (("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
          ("positions", positions, (B, T), torch.int32)))
-    _kv8_call("lwm_kv8_write", lib().lwm_kv8_write, dev, stream, (
+    _kv8_call("lwm_kv8_write", lib().lwm_kv8_write, dev, (
         k.data_ptr(), v.data_ptr(), positions.data_ptr(), start.data_ptr(),
         None if n_new is None else n_new.data_ptr(), table.data_ptr(),
         table.shape[0], B, T, L, H, D, DTYPE_BF16, code,
@@ -766,7 +779,8 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None, stream=None,
     return cache
 
 
-def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
+@_on_stream
+def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None):
     """Slots start[b] .. start[b] + T - 1 of the cache as (k_rot, v) bf16
     [B,T,H,D], zeros outside [0, min(kv_len[b], L)); the layout fwd_block
     takes rotated keys and values in."""
@@ -784,7 +798,7 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
         k_rot = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
     if v is None:
         v = torch.empty_like(k_rot)
-    _kv8_call("lwm_kv8_read", lib().lwm_kv8_read, dev, stream, (
+    _kv8_call("lwm_kv8_read", lib().lwm_kv8_read, dev, (
         cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
         cache.v_scale.data_ptr(), start.data_ptr(),
         None if kv_len is None else kv_len.data_ptr(), B, T, L, H, D,
@@ -792,8 +806,9 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     return k_rot, v
 
 
+@_on_stream
 def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
-               n_recent=1, blocks=None, scores=None, stream=None,
+               n_recent=1, blocks=None, scores=None,
                rope_layout="interleaved"):
     """The ``n_select`` blocks of 128 slots per (row, cache head) whose key
     bounds admit the largest scores for q [B,Hq,D]: (blocks int32, scores
@@ -816,7 +831,7 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
         blocks = kv_len.new_empty(lists)
     if scores is None:
         scores = cache.k_scale.new_empty(lists)
-    _kv8_call("lwm_kv8_select", lib().lwm_kv8_select, dev, stream, (
+    _kv8_call("lwm_kv8_select", lib().lwm_kv8_select, dev, (
         q.data_ptr(), cache.k_bounds.data_ptr(), cache.k_scale.data_ptr(),
         kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
         table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
@@ -830,8 +845,9 @@ def kv8_decode_workspace_size(B, L, Hq, H, n_blocks=None, D=HEAD_DIM) -> int:
         B, L, Hq, H, D, -1 if n_blocks is None else n_blocks))
 
 
+@_on_stream
 def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
-               out=None, lse=None, workspace=None, stream=None,
+               out=None, lse=None, workspace=None,
                rope_layout="interleaved"):
     """One query token per (row, head), q [B,Hq,D], against slots
     [kv_start[b], kv_len[b]) of an 8-bit cache, or only those of ``blocks``
@@ -864,7 +880,7 @@ def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
         out = torch.empty_like(q)
     if lse is None:
         lse = cache.k_scale.new_empty((B, Hq))
-    _kv8_call("lwm_kv8_decode", C.lwm_kv8_decode, dev, stream, (
+    _kv8_call("lwm_kv8_decode", C.lwm_kv8_decode, dev, (
         q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
         kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),

@@ -163,6 +163,8 @@ def check_write(c, kind, layout, T, start, n_new=None, seed=3, scale=1.0):
     (300, 1, [299, 300, -1, 200, 64], None),         # ragged last block
     (700, 300, [77, 0, 401, 690, -40], None),
     (515, 130, [0, 126, 3, 380, 500], [130, 0, 1, 77, 500]),
+    (300, 16, [120, 0, 113, 290, -9], [16, 3, 16, 16, 16]),
+    (300, 17, [120, 0, 112, 290, -9], [17, 1, 17, 16, 17]),
     (2000, 900, [1000, 5, 640, 1100, 127], [900, 899, 256, 900, -3]),
 ])
 def test_write_matches_the_definition(cuda_dev, kind, layout, L, T, start,
@@ -377,6 +379,22 @@ def test_decode_many_short_rows(cuda_dev, kind):
     check_decode(c, q, pos, table, s.tolist(), n.tolist(), "half")
 
 
+@pytest.mark.parametrize("B", [1, 400])
+def test_decode_of_rows_that_all_see_nothing(cuda_dev, B):
+    c = filled(B, 130, 2, "e4m3", seed=11)
+    q, pos, table = queries(B, 4, 130, 11)
+    z = torch.zeros((B,), dtype=torch.int32, device="cuda")
+    for kw in ({}, {"blocks": torch.empty((B, 2, 0), dtype=torch.int32,
+                                          device="cuda")}):
+        # (the list is empty though the range is not)
+        end = z + 130 if kw else z
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full((B, 4), float("nan"), device="cuda")
+        ops.kv8_decode(q, c, z, end, pos, table, out=out, lse=lse, **kw)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and (lse == -float("inf")).all()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("scale", [8.0, 60.0])
 def test_decode_peaked_softmax(cuda_dev, kind, scale):
@@ -523,6 +541,19 @@ def test_select_matches_the_definition(cuda_dev, kind, H, G, layout, L, K):
     check_select(c, q, pos, table, [0, L // 3 + 1], [L, L - 77], K, layout)
 
 
+def test_select_of_the_longest_row(cuda_dev):
+    L = 1 << 22
+    n = L // 128
+    g = torch.Generator("cuda").manual_seed(9)
+    c = ops.kv8_cache(1, L, 1, dtype=torch.int8)
+    b = torch.randint(-127, 128, c.k_bounds.shape, dtype=torch.int8,
+                      device="cuda", generator=g)
+    c.k_bounds.copy_(torch.sort(b, dim=-2).values)
+    c.k_scale.copy_(torch.rand((1, 1, n), device="cuda", generator=g))
+    q, pos, table = queries(1, 3, 4000, 39)
+    check_select(c, q, pos, table, [1000], [L - 1], 3000, "half", 4, 100)
+
+
 @pytest.mark.parametrize("start,length,K,sink,recent", [
     ([0, 0], [0, 1], 2, 1, 1), ([500, 127], [500, 129], 2, 1, 1),
     ([0, 300], [3000, 301], 64, 4, 8),          # fewer blocks than K
@@ -663,6 +694,16 @@ def test_graph_replay_and_another_stream(cuda_dev):
         step(res)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(flat(res), keep))
+    # the stream given to the calls instead
+    ops.kv8_write(c, k, v, pos[:, None].contiguous(), at, table, stream=side)
+    bl, _ = ops.kv8_select(q, c, z, n, pos, table, 8, stream=side)
+    res = {"blocks": bl, "sparse": ops.kv8_decode(q, c, z, n, pos, table,
+                                                  blocks=bl, stream=side),
+           "dense": ops.kv8_decode(q, c, z, n, pos, table, stream=side)}
+    kr, _ = ops.kv8_read(c, at, 1, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(flat(res), keep))
+    assert torch.equal(kr, ops.kv8_read(c, at, 1)[0])
 
 
 def test_offsets_past_32_bits(cuda_dev):

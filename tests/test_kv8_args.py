@@ -69,6 +69,7 @@ INV, UNS, WSP = ops.ERR_INVALID_ARG, ops.ERR_UNSUPPORTED, ops.ERR_WORKSPACE
     (read, {"D": 256}, UNS), (read, {"dtype": 1}, UNS),
     (read, {"T": 0, "k": None}, ops.OK), (read, {"B": 0}, ops.OK),
     (select, {"kb": None}, INV), (select, {"scores": OFF}, INV),
+    (select, {"H": 0}, INV), (decode, {"H": 0}, INV),   # heads over none
     (select, {"Hq": 5}, INV), (select, {"Hq": -2}, INV),
     (select, {"K": 0}, INV), (select, {"sink": -1}, INV),
     (select, {"sink": 2, "recent": 1}, INV),        # more than K
@@ -101,6 +102,7 @@ def test_workspace_size_counts_partial_results():
     assert size(1, 4096, 8, 2, 64, -1) == 0
     assert size(-1, 4096, 8, 2, 128, -1) == 0
     assert size(0, 4096, 8, 2, 128, -1) == 0
+    assert size(1, 4096, 8, 0, 128, -1) == 0
 
 
 def _refused(fn, *a, **kw):
