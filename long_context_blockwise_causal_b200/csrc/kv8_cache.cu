@@ -80,9 +80,13 @@ __device__ __forceinline__ void rotate(float& x, float& y, float c, float s) {
 // (two pairs of the rotation: adjacent channels, or channels 64 apart). The
 // tokens are taken twice, for the maximum and for the codes; the usual
 // append of a token that leaves the scale alone reads the token, the scale
-// and 256 bounds and writes 128 codes. Bound by latency.
+// and 256 bounds and writes 128 codes. Bound by latency: one token of 8 to
+// 512 (row, head) pairs takes 2.3 to 2.7 us, where the kernel for many
+// tokens takes 5.7 to 16; 8 tokens 4.6 to 5.8 against 5.8 to 16, 16 tokens
+// 7.2 to 9.4 against 5.9 to 16, and from 32 on it loses (11 to 16 against 6
+// to 25). So it is taken up to 12 tokens.
 constexpr int kFewThreads = 128;
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 12;
 
 template <bool kInt8, bool kHalf>
 __global__ void __launch_bounds__(kFewThreads)
@@ -240,15 +244,19 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
 //
 // A CTA takes a block of 128 slots for a run of heads: K of all of them,
 // then V. The heads' [128 tokens][128] bf16 boxes come in by TMA through a
-// ring of stages, the angles of the block's tokens (512 bytes each, any
-// positions) by one bulk copy per token, while V of the block before is
-// worked on. Two groups of eight warps take the boxes in turn, so that one
-// computes while the other waits. 16 lanes share a token, eight channels
-// each (4c .. 4c + 3 and the same 64 further up), eight tokens per thread;
-// the rotated block stays in registers between the maximum and the
-// encoding, so each input is read once and each code written once. K keeps
-// the channels' smallest and largest value, which give the block's maximum
-// as well as its bounds. One barrier of the group per box.
+// ring of stages, the angles of the block's tokens (512 bytes each) by bulk
+// copies while V of the block before is worked on. Two groups of eight warps
+// take the boxes in turn, so that one computes while the other waits. 16
+// lanes share a token, eight channels each (4c .. 4c + 3 and the same 64
+// further up), eight tokens per thread; the rotated block stays in registers
+// between the maximum and the encoding, so each input is read once and each
+// code written once. K keeps the channels' smallest and largest value, which
+// give the block's maximum as well as its bounds. One barrier of the group
+// per box.
+// The traffic alone takes 124 us for 32K tokens x 32 heads (805 MB at the
+// rate of a copy); this takes 156, most of what is left being K's rotation
+// and ranges. One group of 16 warps, the angles in registers, took 187; the
+// first form, a CTA per block and head without TMA, 536.
 constexpr int kWrGroups = 2;
 constexpr int kWrGroup = 256;                       // threads of a group
 constexpr int kWrWarps = kWrGroup / 32;

@@ -163,8 +163,8 @@ def check_write(c, kind, layout, T, start, n_new=None, seed=3, scale=1.0):
     (300, 1, [299, 300, -1, 200, 64], None),         # ragged last block
     (700, 300, [77, 0, 401, 690, -40], None),
     (515, 130, [0, 126, 3, 380, 500], [130, 0, 1, 77, 500]),
-    (300, 16, [120, 0, 113, 290, -9], [16, 3, 16, 16, 16]),
-    (300, 17, [120, 0, 112, 290, -9], [17, 1, 17, 16, 17]),
+    (300, 12, [120, 0, 117, 290, -9], [12, 3, 12, 12, 12]),
+    (300, 13, [120, 0, 116, 290, -9], [13, 1, 13, 12, 13]),
     (2000, 900, [1000, 5, 640, 1100, 127], [900, 899, 256, 900, -3]),
 ])
 def test_write_matches_the_definition(cuda_dev, kind, layout, L, T, start,
