@@ -139,17 +139,27 @@ __host__ __device__ constexpr int part_stride(int G) {
 // Q and P become codes of the cache's type: a number is the sum of a few
 // codes (terms), each carrying what the ones before it left, and each term
 // of each head is one column n; products of codes are exact and the columns
-// are added up in fp32. e4m3: terms 1/16 apart, 5 for q (2^-20 of a channel),
-// 3 for p (2^-12 of a weight). int8: terms 1/128 apart, 3 for q and 3 for p
-// (2^-21 of the largest). Weights are taken against the tile's own maximum,
-// so what a term cannot hold is small against the tile's own sum, however
-// far the running maximum lies above it.
+// are added up in fp32. e4m3: terms 1/16 apart, 5 for q (2^-20 of a channel,
+// or 2^-34 of the largest), 3 for p (2^-12 of a weight, or 2^-26 of the
+// largest). int8: terms 1/254 apart, 3 for q (2^-22 of the largest channel)
+// and 3 for p (2^-24 of the largest weight). Weights are taken against the
+// tile's own maximum, so what the terms cannot hold is small against the
+// tile's own sum, however far the running maximum lies above it.
 //
-// Softmax warps: four per group of at most 8 heads; thread t of a group is slot
-// t of S (scores, maximum, weights) and channel t of O (accumulator). The
-// warp after them issues the products, the last one walks the tiles and
+// Softmax warps: four per group of at most 8 heads; thread t of a group is
+// slot t of S (scores, maximum, weights) and channel t of O (accumulator).
+// The warp after them issues the products, the last one walks the tiles and
 // loads them by TMA. The products of one tile run while the softmax works
 // on the next: S, P and O are double buffered.
+//
+// Bound by HBM (256 bytes per slot and cache head) up to 8 query heads per
+// cache head: a 1M-slot cache of 32 heads in 1.16 ms (7.4 TB/s), 16 rows x
+// 32K x 8 heads in 161 us with 1 to 4 query heads each (6.7 TB/s) and 175 to
+// 181 with 8 (6.0); with 16 the softmax warps bound it (290 to 330 us). A
+// kernel that decoded the codes on the CUDA cores took 18.8 ms for the
+// 1M-slot cache. What a call costs beside the traffic is about 8 us: the
+// walk to the first tile and its query (5 us to the first scores), the last
+// tile's product, and joining the parts (3 us).
 constexpr int kDecRing = 8;              // tile descriptions
 constexpr uint64_t kDecWaitNs = 4000000000ull;
 constexpr int kTile = kKv8Block * kHeadDim;   // bytes of K or V of one tile

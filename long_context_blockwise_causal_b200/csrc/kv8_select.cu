@@ -104,7 +104,9 @@ __device__ __forceinline__ int sum16(int (&v)[N]) {
 // three rounds over 8 CTAs) than one CTA takes for everything. Scoring is
 // bound by reading the bounds (256 bytes per block): 16 lanes share a block,
 // a warp keeps several pairs of blocks in flight, the first of them while
-// the query is made ready. GP: G rounded up to a power of two.
+// the query is made ready: 1M slots x 32 heads (67 MB) in 18 us, of which
+// scoring 16 and choosing 512 of 8192 blocks 2; 4 rows x 8 heads x 32K with
+// 4 query heads each in 6.7 us (latency). GP: G rounded up to a power of two.
 template <int GP, int Threads>
 struct Sel {
   // 512 threads, one CTA per SM, for few long rows; 256 threads, four CTAs
@@ -475,8 +477,10 @@ cudaError_t launch_rows(const Kv8SelectArgs& a, int C, cudaStream_t st) {
 }
 
 // Few (row, head) pairs: a cluster of large CTAs each, as long as there are
-// SMs for all of them at once and 128 blocks for each. Many pairs, or short
-// rows: one small CTA each, four to an SM.
+// SMs for all of them at once and 128 blocks for each (32 heads of 1M slots:
+// 26 us over clusters of 4 where clusters of 8, in two rounds, took 37).
+// Many pairs, or short rows: one small CTA each, four to an SM (16 rows x 32
+// heads x 32K: 11.5 us; two large ones to an SM took 17.8).
 template <int GP>
 cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
