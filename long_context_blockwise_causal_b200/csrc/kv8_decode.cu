@@ -653,12 +653,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         const float m = fmaxf(fmaxf(w[0], w[GP]),
                               fmaxf(w[2 * GP], w[3 * GP]));
         const bool fine = m <= 3.402823466e38f;
-        // m < 2^e
+        // m < 2^e; the factor 2^k is exact, and so are its products
         const int e = int(__float_as_uint(m) >> 23) - 126;
-        y[g] = fine ? ldexpf(x[g], C::kQExp - e) : 0.f;
+        const int k = min(C::kQExp - e, 126);
+        y[g] = fine ? x[g] * __uint_as_float(uint32_t(127 + k) << 23) : 0.f;
         if (t == 0)
           qscale[buf * GP + h0 + g] =
-              fine ? ldexpf(kLog2e / sqrtf(float(kHeadDim)), e - C::kQExp)
+              fine ? kLog2e / sqrtf(float(kHeadDim)) *
+                         __uint_as_float(uint32_t(127 - k) << 23)
                    : __int_as_float(0x7fffffff);
       }
       uint8_t* dst = smem + C::kQ;
