@@ -445,7 +445,12 @@ LWM_API int lwm_blockattn_decode(const void* q, const void* k_rot,
  * Keys are stored rotated, in the rope_layout they came in. Scales of
  * blocks that were never written should be 0 (a zeroed cache is a valid
  * empty one). Query heads: Hq a multiple of H, at most 16 per cache head;
- * query head i reads cache head i / (Hq / H). */
+ * query head i reads cache head i / (Hq / H).
+ * Sizes: B * L and B * T of at most 2^31 - 128, B * H below 2^28 (else
+ * LWM_ERR_INVALID_ARG). LWM_ERR_UNSUPPORTED is returned for more heads per
+ * cache head, for a write that can touch 2^31 blocks of all heads, K and V,
+ * a read of 2^29 and a decode over 2^31 - 4096 listed or cached blocks of
+ * all rows and heads. */
 typedef enum { LWM_KV8_E4M3 = 0, LWM_KV8_INT8 = 1 } lwm_kv8_type;
 
 /* Rotates and quantises new tokens into the cache.

@@ -17,6 +17,15 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kInt8Max = 127.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // smaller scales become 0
 
+// Reads what the kernel before may have written (a cache's scales, bounds and
+// codes, a row's length). That kernel can still run when this one begins, so
+// the read-only path, whose data must hold from a kernel's start to its end,
+// is not for it: these are plain loads behind pdl_wait().
+template <typename T>
+__device__ __forceinline__ T ld_now(const T* p) {
+  return *p;
+}
+
 struct Kv8WriteArgs {
   const void* x[2];            // k, v: bf16 [B][T][H][128], un-rotated
   void* codes[2];

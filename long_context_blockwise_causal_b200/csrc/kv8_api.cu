@@ -27,10 +27,14 @@ bool words_ok(std::initializer_list<const void*> ps) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? LWM_OK : LWM_ERR_CUDA; }
 
+// Slots or tokens of all rows are counted in 32 bits, rounded up to blocks.
+constexpr int64_t kMostSlots = (int64_t(1) << 31) - kKv8Block;
+
 // Sizes that every call shares. Slots, blocks and (row, head) pairs are
 // counted in 32 bits; bytes in 64.
 int cache_status(int B, int L, int H, int D, int cache_type) {
-  if (B < 0 || L < 0 || H < 0 || int64_t(B) * L >= (int64_t(1) << 31) ||
+  if (B < 0 || L < 0 || H < 0 || int64_t(B) * L > kMostSlots ||
+      L > kMostSlots ||
       int64_t(B) * H >= (int64_t(1) << 28))
     return LWM_ERR_INVALID_ARG;
   if (cache_type != LWM_KV8_E4M3 && cache_type != LWM_KV8_INT8)
@@ -68,7 +72,7 @@ int lwm_kv8_write(const void* k, const void* v, const int32_t* positions,
                   float* v_scale, int8_t* k_bounds, void* stream) {
   int s = cache_status(B, L, H, D, cache_type);
   if (s != LWM_OK) return s;
-  if (T < 0 || max_pos < 0 || int64_t(B) * T >= (int64_t(1) << 31) ||
+  if (T < 0 || max_pos < 0 || int64_t(B) * T > kMostSlots ||
       (rope_layout != LWM_ROPE_INTERLEAVED && rope_layout != LWM_ROPE_HALF))
     return LWM_ERR_INVALID_ARG;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
@@ -111,7 +115,7 @@ int lwm_kv8_read(const void* k_cache, const void* v_cache,
                  void* v, void* stream) {
   int s = cache_status(B, L, H, D, cache_type);
   if (s != LWM_OK) return s;
-  if (T < 0 || int64_t(B) * T >= (int64_t(1) << 31))
+  if (T < 0 || int64_t(B) * T > kMostSlots)
     return LWM_ERR_INVALID_ARG;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;
   if (int64_t(B) * H == 0 || T == 0) return LWM_OK;

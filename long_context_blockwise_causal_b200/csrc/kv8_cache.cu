@@ -26,8 +26,8 @@ struct NewSlots {
 };
 __device__ __forceinline__ NewSlots new_slots(const Kv8WriteArgs& a, int b) {
   NewSlots n;
-  n.start = __ldg(a.start + b);
-  const int count = a.n_new ? max(0, min(__ldg(a.n_new + b), a.T)) : a.T;
+  n.start = ld_now(a.start + b);
+  const int count = a.n_new ? max(0, min(ld_now(a.n_new + b), a.T)) : a.T;
   n.lo = n.start > 0 ? n.start : 0;
   n.hi = min(n.start + count, int64_t(a.L));
   return n;
@@ -123,16 +123,16 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
   auto load = [&](int r) {
     const int64_t tok = int64_t(b) * a.T + (base + r - ns.start);
     const char* row = x_all + (tok * a.H + h) * (kHeadDim * 2);
-    const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(row + 2 * c0));
-    const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(row + 2 * c1));
+    const uint32_t w0 = ld_now(reinterpret_cast<const uint32_t*>(row + 2 * c0));
+    const uint32_t w1 = ld_now(reinterpret_cast<const uint32_t*>(row + 2 * c1));
     x[0] = bf16lo_to_f32(w0);
     x[1] = bf16hi_to_f32(w0);
     x[2] = bf16lo_to_f32(w1);
     x[3] = bf16hi_to_f32(w1);
     if (key) {
-      const int p = max(0, min(__ldg(a.positions + tok), a.max_pos - 1));
+      const int p = max(0, min(ld_now(a.positions + tok), a.max_pos - 1));
       // pairs 2 lane and 2 lane + 1
-      const float4 cs = __ldg(reinterpret_cast<const float4*>(
+      const float4 cs = ld_now(reinterpret_cast<const float4*>(
                                   a.table + int64_t(p) * kHeadDim) + lane);
       if (kHalf) {
         rotate(x[0], x[2], cs.x, cs.y);
@@ -582,11 +582,11 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int k = 0; k < kKv8Block / 32; ++k) {
         const int r = lane + 32 * k;
         p[k] = r >= lo && r < hi
-                   ? max(0, min(__ldg(pos + r), a.max_pos - 1))
+                   ? max(0, min(ld_now(pos + r), a.max_pos - 1))
                    : -1;
       }
       const int first =
-          max(0, min(__ldg(pos + lo), a.max_pos - 1)) - lo;   // of slot 0
+          max(0, min(ld_now(pos + lo), a.max_pos - 1)) - lo;   // of slot 0
       bool run = true;
 #pragma unroll
       for (int k = 0; k < kKv8Block / 32; ++k)
@@ -711,14 +711,14 @@ kv8_read_kernel(const __grid_constant__ Kv8ReadArgs a, int tiles) {
   if (tok >= a.T) return;
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
   const int64_t bh = int64_t(b) * a.H + h;
-  const int64_t slot = int64_t(__ldg(a.start + b)) + tok;
-  const int len = a.kv_len ? min(__ldg(a.kv_len + b), a.L) : a.L;
+  const int64_t slot = int64_t(ld_now(a.start + b)) + tok;
+  const int len = a.kv_len ? min(ld_now(a.kv_len + b), a.L) : a.L;
   uint4 w = make_uint4(0, 0, 0, 0);
   float s = 0.f;
   if (slot >= 0 && slot < len) {
-    w = __ldg(static_cast<const uint4*>(key ? a.codes[0] : a.codes[1]) +
+    w = ld_now(static_cast<const uint4*>(key ? a.codes[0] : a.codes[1]) +
               (bh * a.L + slot) * 8 + c);
-    s = __ldg((key ? a.scale[0] : a.scale[1]) + bh * nblk + slot / kKv8Block);
+    s = ld_now((key ? a.scale[0] : a.scale[1]) + bh * nblk + slot / kKv8Block);
   }
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[8];

@@ -40,8 +40,8 @@ struct RowTiles {
 
 __device__ __forceinline__ RowTiles row_tiles(const Rows& r, int b) {
   RowTiles x;
-  const int len = __ldg(r.kv_len + b), start = __ldg(r.kv_start + b);
-  const int pos = __ldg(r.q_pos + b);
+  const int len = ld_now(r.kv_len + b), start = ld_now(r.kv_start + b);
+  const int pos = ld_now(r.q_pos + b);
   x.len = max(0, min(len, r.L));
   x.start = max(0, min(start, x.len));
   x.pos = max(0, min(pos, r.max_pos - 1));
@@ -394,9 +394,9 @@ struct Walker {
       if (rows.listed) {
         const int32_t* list =
             blocks + (int64_t(b) * rows.H + h) * rows.K;
-        blk = __ldg(list + j);
+        blk = ld_now(list + j);
         ok = blk >= rt.t0 && int64_t(blk) * kKv8Block < rt.len &&
-             (j == 0 || blk > __ldg(list + j - 1));
+             (j == 0 || blk > ld_now(list + j - 1));
       }
       ++j;
       if (!ok) continue;
@@ -611,7 +611,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     const bool low = a.half ? t < 64 : (t & 1) == 0;
     auto fetch_q = [&](const Tile& x) {
       const int k = a.half ? (t & 63) : (t >> 1);
-      q_cs = __ldg(reinterpret_cast<const float2*>(a.table) +
+      q_cs = ld_now(reinterpret_cast<const float2*>(a.table) +
                    int64_t(x.pos) * (kHeadDim / 2) + k);
       const uint16_t* q = static_cast<const uint16_t*>(a.q) +
                           ((int64_t(x.b) * a.H + x.h) * a.G + h0) * kHeadDim;
@@ -620,9 +620,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         q_raw[g] = 0;
         if (h0 + g >= a.G) continue;
         const uint16_t* row = q + g * kHeadDim;
-        q_raw[g] = a.half
-                       ? __ldg(row + k) | (uint32_t(__ldg(row + k + 64)) << 16)
-                       : __ldg(reinterpret_cast<const uint32_t*>(row) + k);
+        q_raw[g] =
+            a.half ? ld_now(row + k) | (uint32_t(ld_now(row + k + 64)) << 16)
+                   : ld_now(reinterpret_cast<const uint32_t*>(row) + k);
       }
     };
     // ... then rotated and split into terms. Called when the scores of the
@@ -702,8 +702,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
     auto fetch = [&](const Tile& x) {
       if (x.lo >= x.hi) return;
       const int64_t i = (int64_t(x.b) * a.H + x.h) * nblk + x.blk;
-      ks_next = __ldg(a.k_scale + i);
-      vs_next = __ldg(a.v_scale + i);
+      ks_next = ld_now(a.k_scale + i);
+      vs_next = ld_now(a.v_scale + i);
     };
     if (go && !(cur.flags & kEnd)) {
       fetch_q(cur);

@@ -142,8 +142,8 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   pdl_wait();
   pdl_trigger();
 
-  const int len = max(0, min(__ldg(a.kv_len + b), a.L));
-  const int start = max(0, min(__ldg(a.kv_start + b), len));
+  const int len = max(0, min(ld_now(a.kv_len + b), a.L));
+  const int start = max(0, min(ld_now(a.kv_start + b), len));
   const int j0 = start / kKv8Block;
   const int j1 = len > start ? (len + kKv8Block - 1) / kKv8Block : j0;
   const int nv = j1 - j0;
@@ -163,7 +163,7 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
       const int blk = i + f * kSelWarps * 2 + (lane >> 4);
       w[f] = make_int4(0, 0, 0, 0);
       if (blk < n)
-        w[f] = __ldg(reinterpret_cast<const int4*>(
+        w[f] = ld_now(reinterpret_cast<const int4*>(
             bounds + int64_t(blk) * (2 * kHeadDim)));
     }
   };
@@ -171,7 +171,7 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
 
   // query codes: qc[g] = (min(qi, 0), max(qi, 0)), as the bounds lie; a warp
   // per head, two pairs of the rotation per lane
-  const int p = max(0, min(__ldg(a.q_pos + b), a.max_pos - 1));
+  const int p = max(0, min(ld_now(a.q_pos + b), a.max_pos - 1));
   for (int g = warp; g < GP; g += kSelWarps) {
     const int c0 = a.half ? 2 * lane : 4 * lane;       // channels c0, c0 + 1,
     const int c1 = a.half ? 64 + 2 * lane : c0 + 2;    // c1, c1 + 1
@@ -179,9 +179,9 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
     if (g < a.G) {
       const char* q = static_cast<const char*>(a.q) +
                       (bh * a.G + g) * (kHeadDim * 2);
-      const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(q + 2 * c0));
-      const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(q + 2 * c1));
-      const float4 cs = __ldg(reinterpret_cast<const float4*>(
+      const uint32_t w0 = ld_now(reinterpret_cast<const uint32_t*>(q + 2 * c0));
+      const uint32_t w1 = ld_now(reinterpret_cast<const uint32_t*>(q + 2 * c1));
+      const float4 cs = ld_now(reinterpret_cast<const float4*>(
                                   a.table + int64_t(p) * kHeadDim) + lane);
       const double f[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0),
                            bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
@@ -246,7 +246,7 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
         const int first = i + f0 * kSelWarps * 2;
         if (first >= n) break;
         const int blk = first + my_pair * kSelWarps * 2 + (lane >> 4);
-        const float s = blk < n ? __ldg(ks + blk) : 0.f;
+        const float s = blk < n ? ld_now(ks + blk) : 0.f;
         int dot[kSums];
 #pragma unroll
         for (int g = 0; g < GP; ++g) {

@@ -73,6 +73,11 @@ INV, UNS, WSP = ops.ERR_INVALID_ARG, ops.ERR_UNSUPPORTED, ops.ERR_WORKSPACE
     (select, {"Hq": 5}, INV), (select, {"Hq": -2}, INV),
     (select, {"K": 0}, INV), (select, {"sink": -1}, INV),
     (select, {"sink": 2, "recent": 1}, INV),        # more than K
+    (write, {"L": 2 ** 31 - 1, "H": 1}, INV), (write, {"T": 2 ** 31 - 1}, INV),
+    (read, {"L": 2 ** 31 - 127, "H": 1}, INV), (read, {"T": 2 ** 31 - 1}, INV),
+    (decode, {"L": 2 ** 31 - 1, "H": 1}, INV),
+    (decode, {"B": 1 << 12, "L": 128, "H": 1, "Hq": 1, "K": 1 << 19}, UNS),
+    (read, {"B": 1 << 20, "H": 1 << 7, "L": 128}, UNS),
     (select, {"sink": 2 ** 31 - 1, "recent": 2 ** 31 - 1}, INV),
     (select, {"max_pos": 0}, INV), (select, {"layout": 7}, INV),
     (select, {"Hq": 34}, UNS), (select, {"D": 64}, UNS),
