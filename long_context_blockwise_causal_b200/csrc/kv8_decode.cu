@@ -40,8 +40,8 @@ struct RowTiles {
 
 __device__ __forceinline__ RowTiles row_tiles(const Rows& r, int b) {
   RowTiles x;
-  const int len = ld_now(r.kv_len + b), start = ld_now(r.kv_start + b);
-  const int pos = ld_now(r.q_pos + b);
+  const int len = __ldcg(r.kv_len + b), start = __ldcg(r.kv_start + b);
+  const int pos = __ldcg(r.q_pos + b);
   x.len = max(0, min(len, r.L));
   x.start = max(0, min(start, x.len));
   x.pos = max(0, min(pos, r.max_pos - 1));
@@ -908,14 +908,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
 // a row that sees nothing. A pass takes up to 64 parts: their maxima and
 // sums by one thread each, their accumulators by eight groups of 32 lanes
 // (four channels per lane), every group an eighth of the parts.
+// Which parts they are follows from the rows' lengths, which are read before
+// pdl_wait(), while the last tiles are worked on: every CTA of the decode
+// kernel has waited for the work before it when it lets this kernel begin,
+// so they are final then, in L2, where row_tiles() reads them.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinGroups = kJoinThreads / 32;
 constexpr int kJoinParts = 64;
 
 __global__ void __launch_bounds__(kJoinThreads)
 kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
-  pdl_wait();
-  pdl_trigger();
   __shared__ int where[2];
   __shared__ float wt[kJoinParts];
   __shared__ float4 part[kJoinGroups][32];
@@ -929,6 +931,9 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
     if (lane == 0) where[warp] = n;
   }
   const int n = row_tiles(rows, b).n;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                        int64_t(blockIdx.x) * kHeadDim;
   if (n == 0) {
@@ -936,7 +941,6 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
     if (t == 0) a.lse[blockIdx.x] = -INFINITY;
     return;
   }
-  __syncthreads();
   const Shares sh(where[0], C);
   const int p0 = where[1] + h * n;
   const int c0 = sh.holder(p0), c1 = sh.holder(p0 + n - 1);
@@ -967,8 +971,8 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int j = lane + 32 * i;
-      mp[i] = j < k ? record(c + j)[g] : -INFINITY;
-      lp[i] = j < k ? record(c + j)[a.G + g] : 0.f;
+      mp[i] = j < k ? __ldcg(record(c + j) + g) : -INFINITY;
+      lp[i] = j < k ? __ldcg(record(c + j) + a.G + g) : 0.f;
       mx = fmaxf(mx, mp[i]);
     }
     mx = warp_max(mx);
@@ -1022,8 +1026,6 @@ kv8_combine_kernel(const Kv8DecodeArgs a, int C) {
 // tile first(c); the pair it runs through is joined at its first cut.
 __global__ void __launch_bounds__(kJoinThreads)
 kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
-  pdl_wait();
-  pdl_trigger();
   __shared__ Start at;
   __shared__ int tiles;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1036,6 +1038,9 @@ kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
     const int n = tiles_before(rows, a.B) * a.H;
     if (lane == 0) tiles = n;
   }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   // rows that see nothing
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (row_tiles(rows, b).n > 0) continue;
@@ -1045,7 +1050,6 @@ kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
     for (int i = t; i < a.H * a.G; i += kJoinThreads)
       a.lse[q0 + i] = -INFINITY;
   }
-  __syncthreads();
   // a call of one CTA has no cut; and there may be no tiles behind one
   if (int(blockIdx.x) + 1 >= C || at.u0 >= at.u1) return;
   const Shares sh(tiles, C);
