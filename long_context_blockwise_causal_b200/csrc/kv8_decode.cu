@@ -154,12 +154,12 @@ __host__ __device__ constexpr int part_stride(int G) {
 //
 // Bound by HBM (256 bytes per slot and cache head) up to 8 query heads per
 // cache head: a 1M-slot cache of 32 heads in 1.16 ms (7.4 TB/s), 16 rows x
-// 32K x 8 heads in 161 us with 1 to 4 query heads each (6.7 TB/s) and 175 to
-// 181 with 8 (6.0); with 16 the softmax warps bound it (290 to 330 us). A
-// kernel that decoded the codes on the CUDA cores took 18.8 ms for the
-// 1M-slot cache. What a call costs beside the traffic is about 8 us: the
-// walk to the first tile and its query (5 us to the first scores), the last
-// tile's product, and joining the parts (3 us).
+// 32K x 8 heads in 161 us with 1 to 4 query heads each (6.7 TB/s) and 171 to
+// 173 with 8 (6.3); with 16 the softmax warps' instructions bound it (620 a
+// warp and tile; 233 us, int8 248). A kernel that decoded the codes on the
+// CUDA cores took 18.8 ms for the 1M-slot cache. What a call costs beside
+// the traffic is about 7 us: the walk to the first tile and its query (5 us
+// to the first scores), the last tile's product, and joining the parts (2).
 constexpr int kDecRing = 8;              // tile descriptions
 constexpr uint64_t kDecWaitNs = 4000000000ull;
 constexpr int kTile = kKv8Block * kHeadDim;   // bytes of K or V of one tile
@@ -190,8 +190,7 @@ struct Dec {
   static constexpr int kCols = 2 * kNq + 2 * kNp;
   static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static_assert(kCols <= 256, "CTAs share the SM's 512 columns");
-  // factor from one term to the next, and of the first term
-  static constexpr float kStep = kInt8 ? 254.f : 16.f;
+  // factor of the first term
   static constexpr float kPScale = kInt8 ? 127.f : 256.f;
   static constexpr int kQExp = kInt8 ? 6 : 8;  // |q~| 2^(kQExp - e) < 2^kQExp
   // shared memory, from a 1024-byte boundary
@@ -205,7 +204,7 @@ struct Dec {
   // With three stages, a K tile is refilled together with its V tile: the
   // two then load side by side, 7.4 TB/s from a 1M-token cache, where
   // refilling it as soon as its scores are done gave 7.1. With fewer, the
-  // earlier refill wins (16 heads, 16 x 32K: 300 against 320 us).
+  // earlier refill wins (16 heads, 16 x 32K: 233 against 264 us).
   static constexpr int kRoom = 233472 / kPerSm - 2048 - kSmall;
   static constexpr int kTiles = kRoom / kTile < 6 ? kRoom / kTile : 6;
   static constexpr int kKStages = kTiles / 2, kVStages = kTiles - kKStages;
@@ -230,12 +229,6 @@ struct Dec {
   static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory per SM");
   static_assert(kVStages + 2 < kDecRing, "descriptions outlive their tiles");
 };
-
-// Byte (row, col) of a K-major operand of 128-byte rows, 128-byte swizzle.
-__device__ __forceinline__ int sw128(int row, int col) {
-  return (row >> 3) * 1024 + (row & 7) * 128 +
-         ((((col >> 4) ^ (row & 7)) << 4) | (col & 15));
-}
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
@@ -311,9 +304,84 @@ __device__ constexpr uint32_t idesc8(int N, int a_mn) {
          (uint32_t(a_mn) << 15) | (uint32_t(N >> 3) << 17) | (8u << 24);
 }
 
+// Factor from one term to the next.
+template <bool kInt8>
+constexpr float kStepOf = kInt8 ? 254.f : 16.f;
+
 template <bool kInt8>
 __device__ __forceinline__ float term_value(uint32_t w) {
   return kInt8 ? float(int(w)) : __uint_as_float(w);
+}
+
+// x += y, x *= y and x += y z of N numbers, two at a time where there are
+// two.
+template <int N>
+__device__ __forceinline__ void add_all(float (&x)[N], const float (&y)[N]) {
+  if constexpr (N == 1) x[0] += y[0];
+#pragma unroll
+  for (int g = 0; g + 1 < N; g += 2) {
+    const float2 v = add2(make_float2(x[g], x[g + 1]),
+                          make_float2(y[g], y[g + 1]));
+    x[g] = v.x;
+    x[g + 1] = v.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void mul_all(float (&x)[N], const float (&y)[N]) {
+  if constexpr (N == 1) x[0] *= y[0];
+#pragma unroll
+  for (int g = 0; g + 1 < N; g += 2) {
+    const float2 v = mul2(make_float2(x[g], x[g + 1]),
+                          make_float2(y[g], y[g + 1]));
+    x[g] = v.x;
+    x[g + 1] = v.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void mul_all(float (&x)[N], float y) {
+  float all[N];
+#pragma unroll
+  for (int g = 0; g < N; ++g) all[g] = y;
+  mul_all(x, all);
+}
+template <int N>
+__device__ __forceinline__ void fma_all(float (&x)[N], const float (&y)[N],
+                                        const float (&z)[N]) {
+  if constexpr (N == 1) x[0] = fmaf(y[0], z[0], x[0]);
+#pragma unroll
+  for (int g = 0; g + 1 < N; g += 2) {
+    const float2 v = fma2(make_float2(y[g], y[g + 1]),
+                          make_float2(z[g], z[g + 1]),
+                          make_float2(x[g], x[g + 1]));
+    x[g] = v.x;
+    x[g + 1] = v.y;
+  }
+}
+
+// The numbers whose terms are r[0..N)[g], two at a time where there are two.
+template <bool kInt8, int N, int GH>
+__device__ __forceinline__ void join_terms(const uint32_t (&r)[N][GH],
+                                           float (&x)[GH]) {
+  constexpr float kDown = 1.f / kStepOf<kInt8>;
+#pragma unroll
+  for (int g = 0; g < GH; g += 2) {
+    if constexpr (GH > 1) {
+      float2 v = make_float2(term_value<kInt8>(r[N - 1][g]),
+                             term_value<kInt8>(r[N - 1][g + 1]));
+#pragma unroll
+      for (int n = N - 2; n >= 0; --n)
+        v = fma2(v, make_float2(kDown, kDown),
+                 make_float2(term_value<kInt8>(r[n][g]),
+                             term_value<kInt8>(r[n][g + 1])));
+      x[g] = v.x;
+      x[g + 1] = v.y;
+    } else {
+      x[0] = term_value<kInt8>(r[N - 1][0]);
+#pragma unroll
+      for (int n = N - 2; n >= 0; --n)
+        x[0] = fmaf(x[0], kDown, term_value<kInt8>(r[n][0]));
+    }
+  }
 }
 
 // Barrier of a group of softmax warps; true if all its threads said so.
@@ -331,7 +399,7 @@ __device__ __forceinline__ bool softmax_all(int id, bool mine) {
 // The next term of (a, b): its two codes, and what they leave, scaled up.
 template <bool kInt8>
 __device__ __forceinline__ uint32_t next_term(float& a, float& b) {
-  constexpr float kStep = kInt8 ? 254.f : 16.f;
+  constexpr float kStep = kStepOf<kInt8>;
   if constexpr (kInt8) {
     const float ra = rintf(a), rb = rintf(b);
     const uint32_t w = uint32_t(int(ra) & 255) | (uint32_t(int(rb) & 255) << 8);
@@ -347,6 +415,33 @@ __device__ __forceinline__ uint32_t next_term(float& a, float& b) {
     a = r.x;
     b = r.y;
     return w;
+  }
+}
+
+// Stores a code to (Row + h0, t) of a K-major operand of 128-byte rows,
+// 128-byte swizzle (16-byte column c of row r lies at c ^ (r & 7)); h0 is 0
+// or a multiple of 8, at the address of (h0, t), so that the others are an
+// exclusive or and a constant away. (Worked out for each code, 24 addresses
+// took 150 of a thread's 850 instructions per tile.)
+template <int Row>
+__device__ __forceinline__ void st_code(uint32_t at, uint32_t code) {
+  asm volatile("st.shared.u8 [%0+%2], %1;" ::"r"(at ^ ((Row & 7) << 4)),
+               "r"(code), "n"((Row >> 3) * 1024 + (Row & 7) * 128)
+               : "memory");
+}
+
+// The terms of y[0..GH), heads h0 .. of GP, to rows n GP + h0 .. of an
+// operand.
+template <bool kInt8, int GP, int Terms, int GH, int N = 0, int G = 0>
+__device__ __forceinline__ void st_terms(uint32_t at, float (&y)[GH]) {
+  if constexpr (N < Terms) {
+    float none = 0.f;
+    constexpr bool kTwo = G + 1 < GH;
+    const uint32_t w = next_term<kInt8>(y[G], kTwo ? y[(G + 1) % GH] : none);
+    st_code<N * GP + G>(at, w);
+    if constexpr (kTwo) st_code<N * GP + G + 1>(at, w >> 8);
+    constexpr bool kDone = G + 2 >= GH;
+    st_terms<kInt8, GP, Terms, GH, kDone ? N + 1 : N, kDone ? 0 : G + 2>(at, y);
   }
 }
 
@@ -663,18 +758,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          __uint_as_float(uint32_t(127 - k) << 23)
                    : __int_as_float(0x7fffffff);
       }
-      uint8_t* dst = smem + C::kQ;
-#pragma unroll
-      for (int n = 0; n < C::kQTerms; ++n) {
-#pragma unroll
-        for (int g = 0; g < GH; g += 2) {
-          float dummy = 0.f;
-          const uint32_t w =
-              next_term<kInt8>(y[g], g + 1 < GH ? y[(g + 1) % GH] : dummy);
-          dst[sw128(n * GP + h0 + g, t)] = uint8_t(w);
-          if (g + 1 < GH) dst[sw128(n * GP + h0 + g + 1, t)] = uint8_t(w >> 8);
-        }
-      }
+      st_terms<kInt8, GP, C::kQTerms>(sbase + C::kQ + h0 * kHeadDim + t, y);
       fence_proxy_async_smem();
       // all of wsum has been read and qscale written before anyone goes on
       named_barrier_sync(sync_id, 128);
@@ -724,14 +808,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       lds<GH>(stats_of(i) + GH, al);
       lds<GH>(stats_of(i) + 3 * GH, be);
       tmem_wait_ld();
-#pragma unroll
-      for (int g = 0; g < GH; ++g) {
-        float o = term_value<kInt8>(r[C::kPTerms - 1][g]);
-#pragma unroll
-        for (int n = C::kPTerms - 2; n >= 0; --n)
-          o = fmaf(o, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
-        acc[g] = fmaf(o, be[g], acc[g] * al[g]);
-      }
+      float o[GH];
+      join_terms<kInt8>(r, o);
+      mul_all(acc, al);
+      fma_all(acc, o, be);
       tc_fence_before();
     };
 
@@ -771,14 +851,11 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           tmem_wait_ld();
           tc_fence_before();
           const bool seen = t >= cur.lo && t < cur.hi;
+          join_terms<kInt8>(r, s);
+          mul_all(qs, ks);
+          mul_all(s, qs);
 #pragma unroll
-          for (int g = 0; g < GH; ++g) {
-            float x = term_value<kInt8>(r[C::kQTerms - 1][g]);
-#pragma unroll
-            for (int n = C::kQTerms - 2; n >= 0; --n)
-              x = fmaf(x, 1.f / C::kStep, term_value<kInt8>(r[n][g]));
-            s[g] = seen ? x * (ks * qs[g]) : -INFINITY;
-          }
+          for (int g = 0; g < GH; ++g) s[g] = seen ? s[g] : -INFINITY;
         }
         float* wm = wmax + (i & 1) * 4 * GP + h0;
         float mx = 0.f;
@@ -800,7 +877,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           m = mn;
           if (lane < GH) {
             float* st = stats_of(i) + lane;
-            st[0] = mt == -INFINITY ? 0.f : mt;
+            st[0] = mt == -INFINITY ? 0.f : -mt;
             st[GH] = al;
             st[2 * GH] = be;
             st[3 * GH] = be * (vs * (1.f / C::kPScale));
@@ -813,26 +890,15 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
           lds<GH>(stats_of(i), mt);
           lds<GH>(stats_of(i) + GH, al);
           lds<GH>(stats_of(i) + 2 * GH, be);
+          add_all(s, mt);
 #pragma unroll
-          for (int g = 0; g < GH; ++g) {
-            p[g] = ex2(s[g] - mt[g]);
-            l[g] = fmaf(p[g], be[g], l[g] * al[g]);
-            p[g] *= C::kPScale;
-          }
+          for (int g = 0; g < GH; ++g) p[g] = ex2(s[g]);
+          mul_all(l, al);
+          fma_all(l, p, be);
+          mul_all(p, C::kPScale);
         }
-        uint8_t* dst = smem + C::kP + (i & 1) * C::kPBytes;
-#pragma unroll
-        for (int n = 0; n < C::kPTerms; ++n) {
-#pragma unroll
-          for (int g = 0; g < GH; g += 2) {
-            float dummy = 0.f;
-            const uint32_t w =
-                next_term<kInt8>(p[g], g + 1 < GH ? p[(g + 1) % GH] : dummy);
-            dst[sw128(n * GP + h0 + g, t)] = uint8_t(w);
-            if (g + 1 < GH)
-              dst[sw128(n * GP + h0 + g + 1, t)] = uint8_t(w >> 8);
-          }
-        }
+        st_terms<kInt8, GP, C::kPTerms>(
+            sbase + C::kP + (i & 1) * C::kPBytes + h0 * kKv8Block + t, p);
         if (!kInt8 && group == 0 && (t < cur.lo || t >= cur.hi)) {
           // an unseen slot's weight is 0, but its codes may be NaN
           ok = wait(C::bVFull + i % C::kVStages, i / C::kVStages) && ok;
