@@ -608,9 +608,17 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                       a.table + int64_t(p[k]) * kHeadDim, kHeadDim * 4,
                       bar(wAngles));
       }
-      for (int u = 0; u < 2 * (h1 - h0); ++u, ++n) {
-        const bool key = u < h1 - h0;
-        const int h = key ? h0 + u : h0 + u - (h1 - h0);
+      const int heads = h1 - h0;
+      for (int u = 0; u < 2 * heads; ++u, ++n) {
+        // K 0, K 1; V 0, K 2; K 3, V 1; V 2, K 4; ... V n - 2, V n - 1
+        bool key = u < min(2, heads);
+        int h = u;
+        if (!key) {
+          const int pair = (u >> 1) - 1;
+          key = pair < heads - 2 && ((u ^ pair) & 1) != 0;
+          h = pair >= heads - 2 ? u - heads : key ? pair + 2 : pair;
+        }
+        h += h0;
         const int s = n % kWrStages;
         if (n >= kWrStages) ok = wait(wEmpty + s, n / kWrStages - 1);
         if (!ok) break;
