@@ -33,6 +33,11 @@ __device__ __forceinline__ NewSlots new_slots(const Kv8WriteArgs& a, int b) {
   return n;
 }
 
+// Blocks that a row's new slots lie in.
+__device__ __forceinline__ int new_blocks(const NewSlots& n) {
+  return n.lo < n.hi ? int((n.hi - 1) / kKv8Block - n.lo / kKv8Block) + 1 : 0;
+}
+
 // Scale of a block that had s_old and meets amax.
 template <bool kInt8>
 __device__ __forceinline__ float block_scale(float s_old, float amax) {
@@ -80,13 +85,15 @@ __device__ __forceinline__ void rotate(float& x, float& y, float c, float s) {
 // (two pairs of the rotation: adjacent channels, or channels 64 apart). The
 // tokens are taken twice, for the maximum and for the codes; the usual
 // append of a token that leaves the scale alone reads the token, the scale
-// and 256 bounds and writes 128 codes. Bound by latency: one token of 8 to
-// 512 (row, head) pairs takes 2.3 to 2.7 us, where the kernel for many
-// tokens takes 5.7 to 16; 8 tokens 4.6 to 5.8 against 5.8 to 16, 16 tokens
-// 7.2 to 9.4 against 5.9 to 16, and from 32 on it loses (11 to 16 against 6
-// to 25). So it is taken up to 12 tokens.
+// and 256 bounds and writes 128 codes. Bound by latency, half a microsecond
+// per token: 4 tokens of 8 to 512 (row, head) pairs take 3.1 to 4.3 us, where
+// the kernel for many tokens, which moves a whole block whatever is new in
+// it, takes 5.8 to 14. The two meet at 12 tokens where there are few pairs
+// (8 to 128 pairs: 5.8 to 6.4 against 5.8 to 6.6; 16 tokens 7.0 to 7.7
+// against 5.8 to 6.7) and at 32 where each SM has several (512 pairs: 18.8
+// against 18.2; 2048: 33 against 52; 4096: 77 against 105).
 constexpr int kFewThreads = 128;
-constexpr int kFewTokens = 12;
+constexpr int kFewTokens = 12, kFewTokensOfMany = 32, kManyPairs = 512;
 
 template <bool kInt8, bool kHalf>
 __global__ void __launch_bounds__(kFewThreads)
@@ -242,21 +249,24 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
 
 // ----------------------------------------------------------- many tokens
 //
-// A CTA takes a block of 128 slots for a run of heads: K of all of them,
-// then V. The heads' [128 tokens][128] bf16 boxes come in by TMA through a
-// ring of stages, the angles of the block's tokens (512 bytes each) by bulk
-// copies while V of the block before is worked on. Two groups of eight warps
-// take the boxes in turn, so that one computes while the other waits. 16
-// lanes share a token, eight channels each (4c .. 4c + 3 and the same 64
-// further up), eight tokens per thread; the rotated block stays in registers
-// between the maximum and the encoding, so each input is read once and each
-// code written once. K keeps the channels' smallest and largest value, which
-// give the block's maximum as well as its bounds. One barrier of the group
-// per box.
+// All (row, block of 128 slots, head) that the call touches, in this order,
+// are cut into equal shares, one per CTA, whatever the rows' lengths are.
+// The heads' [128 tokens][128] bf16 boxes, K and V, come in by TMA through a
+// ring of stages, the angles of a block's tokens (512 bytes each) by bulk
+// copies while the last V boxes of the block before are worked on. Two
+// groups of eight warps take the boxes in turn; K and V alternate within
+// each group, so that the instructions of the one and the traffic of the
+// other even out. 16 lanes share a token, eight channels each (4c .. 4c + 3
+// and the same 64 further up), eight tokens per thread; the rotated block
+// stays in registers between the maximum and the encoding, so each input is
+// read once and each code written once. K keeps the channels' smallest and
+// largest value, which give the block's maximum as well as its bounds. One
+// barrier of the group per box.
 // The traffic alone takes 124 us for 32K tokens x 32 heads (805 MB at the
-// rate of a copy); this takes 156, most of what is left being K's rotation
-// and ranges. One group of 16 warps, the angles in registers, took 187; the
-// first form, a CTA per block and head without TMA, 536.
+// rate of a copy); this takes 148, the same without the rotation or the
+// ranges. All K before V took 153, shares of whole runs of heads 164 for the
+// same tokens in 32 rows, one group of 16 warps 187, and a CTA per block and
+// head without TMA 536.
 constexpr int kWrGroups = 2;
 constexpr int kWrGroup = 256;                       // threads of a group
 constexpr int kWrWarps = kWrGroup / 32;
@@ -292,12 +302,6 @@ constexpr int wFull = 0, wEmpty = kWrStages, wAngles = 2 * kWrStages,
               kWrNumBars = wAngles + 1;
 constexpr int kWrSmem = kWrBars + kWrNumBars * 8 + 16 + 128;
 static_assert(kWrSmem <= 232448, "shared memory per CTA");
-
-struct WriteGrid {
-  int per_row;        // blocks a row's tokens can touch
-  int groups, heads;  // head groups and heads in each
-  int64_t items;      // B * per_row * groups
-};
 
 // Barrier of a group; true if all its threads said so.
 __device__ __forceinline__ bool group_all(int id, bool mine) {
@@ -527,8 +531,7 @@ template <bool kInt8, bool kHalf>
 __global__ void __launch_bounds__(kWrThreads, 1)
 kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ Kv8WriteArgs a,
-                 const __grid_constant__ WriteGrid grid, int* status) {
+                 const __grid_constant__ Kv8WriteArgs a, int* status) {
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~uintptr_t(127));
@@ -556,17 +559,55 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
     // -------------------------------------------------------------- loader
     int n = 0, item = 0, last_key = -1;
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < grid.items; i += gridDim.x) {
-      // heads of a block are neighbours
-      const int64_t row_blk = i / grid.groups;
-      const int h0 = int(i - row_blk * grid.groups) * grid.heads;
-      const int h1 = min(h0 + grid.heads, a.H);
-      const int b = int(row_blk / grid.per_row);
-      const NewSlots ns = new_slots(a, b);
+    // rows 32 at a time, one per lane: its new slots, its blocks and those
+    // of the rows up to it, `before` those of the rows below row0
+    NewSlots mine;
+    int count, upto, before = 0, row0 = 0;
+    auto rows_at = [&](int row) {
+      mine = NewSlots{0, 0, 0};
+      if (row + lane < a.B) mine = new_slots(a, row + lane);
+      count = new_blocks(mine);
+      upto = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+    };
+    rows_at(0);
+    int all = __shfl_sync(0xffffffffu, upto, 31);
+    if (a.B > 32) {
+      int more_rows = 0;
+      for (int b = lane + 32; b < a.B; b += 32)
+        more_rows += new_blocks(new_slots(a, b));
+      all += __reduce_add_sync(0xffffffffu, more_rows);
+    }
+    // the CTA's share of all (row, block, head), heads innermost
+    all *= a.H;
+    const int C = gridDim.x, c = blockIdx.x;
+    const int each = all / C, more = all - each * C;
+    int u = each * c + min(c, more);
+    const int u_end = u + each + (c < more);
+    while (ok && u < u_end) {
+      const int blk = u / a.H, h0 = u - blk * a.H;
+      const int heads = min(a.H - h0, u_end - u);
+      uint32_t hit;
+      while ((hit = __ballot_sync(0xffffffffu, blk < before + upto)) == 0 &&
+             row0 + 32 < a.B) {
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        row0 += 32;
+        rows_at(row0);
+      }
+      if (hit == 0) break;
+      const int f = __ffs(hit) - 1, b = row0 + f;
+      NewSlots ns;
+      ns.start = __shfl_sync(0xffffffffu, mine.start, f);
+      ns.lo = __shfl_sync(0xffffffffu, mine.lo, f);
+      ns.hi = __shfl_sync(0xffffffffu, mine.hi, f);
+      const int first_blk = before + __shfl_sync(0xffffffffu, upto - count, f);
       const int64_t base =
-          (ns.lo / kKv8Block + (row_blk - int64_t(b) * grid.per_row)) *
-          kKv8Block;
-      if (ns.lo >= ns.hi || base >= ns.hi) continue;
+          (ns.lo / kKv8Block + (blk - first_blk)) * kKv8Block;
+      u += heads;
       const int lo = int(max(ns.lo - base, int64_t(0)));
       const int hi = int(min(ns.hi - base, int64_t(kKv8Block)));
       const int64_t tok = base - ns.start;   // of the block's first slot
@@ -608,15 +649,14 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                       a.table + int64_t(p[k]) * kHeadDim, kHeadDim * 4,
                       bar(wAngles));
       }
-      const int heads = h1 - h0;
-      for (int u = 0; u < 2 * heads; ++u, ++n) {
+      for (int i = 0; i < 2 * heads; ++i, ++n) {
         // K 0, K 1; V 0, K 2; K 3, V 1; V 2, K 4; ... V n - 2, V n - 1
-        bool key = u < min(2, heads);
-        int h = u;
+        bool key = i < min(2, heads);
+        int h = i;
         if (!key) {
-          const int pair = (u >> 1) - 1;
-          key = pair < heads - 2 && ((u ^ pair) & 1) != 0;
-          h = pair >= heads - 2 ? u - heads : key ? pair + 2 : pair;
+          const int pair = (i >> 1) - 1;
+          key = pair < heads - 2 && ((i ^ pair) & 1) != 0;
+          h = pair >= heads - 2 ? i - heads : key ? pair + 2 : pair;
         }
         h += h0;
         const int s = n % kWrStages;
@@ -758,29 +798,23 @@ cudaError_t launch_many(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
   if (!make_tokens_map(&mk, a.x[0], a.B, a.T, a.H) ||
       !make_tokens_map(&mv, a.x[1], a.B, a.T, a.H))
     return cudaErrorInvalidValue;
-  const int sms = sm_count();
-  WriteGrid g{};
-  g.per_row = (a.T + kKv8Block - 1) / kKv8Block + 1;
-  // as many heads per item as leave each SM six items or more: a longer run
-  // reuses the angles, a shorter one spreads the work
-  const int64_t heads = int64_t(a.B) * g.per_row * a.H;
-  const int most = int(std::max<int64_t>(
-      1, std::min<int64_t>({16, heads / (6 * sms), a.H})));
-  g.groups = (a.H + most - 1) / most;
-  g.heads = (a.H + g.groups - 1) / g.groups;
-  g.items = int64_t(a.B) * g.per_row * g.groups;
   const cudaError_t e = allow_smem<kv8_write_kernel<kInt8, kHalf>>(kWrSmem);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = std::min<int64_t>(g.items, sms);
+  // never more CTAs than there can be (block, head) pairs
+  const int64_t pairs =
+      int64_t(a.B) * a.H * ((a.T + kKv8Block - 1) / kKv8Block + 1);
+  const int64_t ctas = std::min<int64_t>(pairs, sm_count());
   return launch_dependent(kv8_write_kernel<kInt8, kHalf>,
                           dim3(unsigned(ctas)), dim3(kWrThreads), kWrSmem, st,
-                          mk, mv, a, g, status);
+                          mk, mv, a, status);
 }
 
 template <bool kInt8, bool kHalf>
 cudaError_t launch_write(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
-  return a.T <= kFewTokens ? launch_few<kInt8, kHalf>(a, st)
-                           : launch_many<kInt8, kHalf>(a, status, st);
+  const int few = int64_t(a.B) * a.H >= kManyPairs ? kFewTokensOfMany
+                                                   : kFewTokens;
+  return a.T <= few ? launch_few<kInt8, kHalf>(a, st)
+                    : launch_many<kInt8, kHalf>(a, status, st);
 }
 
 }  // namespace

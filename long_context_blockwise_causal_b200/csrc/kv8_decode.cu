@@ -96,7 +96,7 @@ __device__ __forceinline__ Start find_start(const Rows& r, int C, int c) {
   s.b = s.row_at = 0;
   if (s.u0 >= s.u1) return s;
   int base = 0;
-  for (int b0 = 0;; b0 += 32) {     // some row holds u0
+  for (int b0 = 0; b0 < r.B; b0 += 32) {
     if (b0 > 0) {
       mine.n = 0;
       if (b0 + lane < r.B) mine = row_tiles(r, b0 + lane);
@@ -122,6 +122,8 @@ __device__ __forceinline__ Start find_start(const Rows& r, int C, int c) {
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
+  s.u1 = s.u0;   // lengths that change during the call: no work, no fault
+  return s;
 }
 
 // Partial result records: m[G], l[G], padding to 16 bytes, acc[G][128].
@@ -459,7 +461,11 @@ struct Walker {
   __device__ __forceinline__ void open() {   // at tile u < u1
     while (u >= row_at + rt.n * rows.H) {
       row_at += rt.n * rows.H;
-      rt = row_tiles(rows, ++b);
+      if (++b >= rows.B) {     // as in find_start
+        u = u1;
+        return;
+      }
+      rt = row_tiles(rows, b);
     }
     h = (u - row_at) / rt.n;
     const int p0 = row_at + h * rt.n, p1 = p0 + rt.n;

@@ -183,6 +183,23 @@ def test_long_writes_match_the_definition(cuda_dev, kind, layout, H, T, start):
     check_write(c, kind, layout, T, start, [T, T - 131])
 
 
+@pytest.mark.parametrize("T,H", [(150, 7), (32, 8), (33, 8)])
+@pytest.mark.parametrize("kind,layout", [("e4m3", "interleaved"),
+                                         ("int8", "half")])
+def test_writes_of_many_uneven_rows(cuda_dev, kind, layout, T, H):
+    # more rows than a warp takes at once, runs of rows without a new token,
+    # shares that are cut between the heads of a block
+    B, L = 75, 400
+    rng = np.random.default_rng(11)
+    start = rng.integers(-20, L, B)
+    n_new = rng.integers(0, T + 1, B)
+    n_new[3:6] = 0
+    n_new[20:60] = 0
+    start[62], start[63] = L, -T
+    c = filled(B, L, H, kind, seed=1)
+    check_write(c, kind, layout, T, start.tolist(), n_new.tolist())
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_append_raises_a_blocks_scale(cuda_dev, kind):
     # larger tokens each time: the older codes are rounded again
