@@ -673,57 +673,36 @@ def _kv8_group(where, q, H):
     return Hq
 
 
-def _kv8_ready(where, cache, sizes, table, words, wide):
+def _kv8_ready(where, cache, sizes, table, tensors):
     """Shapes, types and placement of every tensor of a call, before any
-    pointer reaches the library: the cache's, the table's, the int32 vectors
-    in `words` (name, tensor or None) of one entry per row, and those of
-    `wide` (name, tensor or None, shape, dtype). Returns the device. These
+    pointer reaches the library: the cache's, the table's and those of
+    `tensors` (name, tensor or None, shape, dtype). Returns the device. These
     calls are short, so the usual case is one pass that finds nothing."""
     B, H, L, D = sizes
     k, v, ks, vs, kb = cache
-    f32, i32 = torch.float32, torch.int32
     n = (L + BLOCK - 1) // BLOCK
-    scales, rows = (B, H, n), (B,)
-    bad = (v.shape != k.shape or v.dtype is not k.dtype
-           or ks.shape != scales or ks.dtype is not f32
-           or vs.shape != scales or vs.dtype is not f32
-           or kb.shape != (B, H, n, 2, D) or kb.dtype is not torch.int8)
-    dev = k.get_device()
-    away = (dev < 0 or v.get_device() != dev or ks.get_device() != dev
-            or vs.get_device() != dev or kb.get_device() != dev)
-    loose = not (k.is_contiguous() and v.is_contiguous()
-                 and ks.is_contiguous() and vs.is_contiguous()
-                 and kb.is_contiguous())
+    scales, dev = (B, H, n), k.get_device()
+    every = (("cache.v", v, k.shape, k.dtype),
+             ("cache.k_scale", ks, scales, torch.float32),
+             ("cache.v_scale", vs, scales, torch.float32),
+             ("cache.k_bounds", kb, (B, H, n, 2, D), torch.int8), *tensors)
     if table is not None:
-        bad |= table.shape[1:] != (D // 2, 2) or table.dtype is not f32
-        away |= table.get_device() != dev
-        loose |= not table.is_contiguous()
-    for _, t in words:
-        if t is not None:
-            bad |= t.shape != rows or t.dtype is not i32
-            away |= t.get_device() != dev
-            loose |= not t.is_contiguous()
-    for _, t, shape, dtype in wide:
-        if t is not None:
-            bad |= t.shape != shape or t.dtype is not dtype
-            away |= t.get_device() != dev
-            loose |= not t.is_contiguous()
-    if bad or away or loose:
-        _expect(where, "cache.v", v, k.shape, k.dtype)
-        _expect(where, "cache.k_scale", ks, scales, f32)
-        _expect(where, "cache.v_scale", vs, scales, f32)
-        _expect(where, "cache.k_bounds", kb, (B, H, n, 2, D), torch.int8)
-        if table is not None:
-            _expect_dims(where, "table", table, 3)
-            _expect(where, "table", table, (table.shape[0], D // 2, 2), f32)
-        for name, t in words:
-            _expect(where, name, t, rows, i32)
-        for name, t, shape, dtype in wide:
-            _expect(where, name, t, shape, dtype)
-        every = (k, v, ks, vs, kb, table, *(t for _, t in words),
-                 *(t for _, t, _, _ in wide))
-        _same_device(where, *every)
-        _need_cuda(*every)
+        _expect_dims(where, "table", table, 3)
+        every += (("table", table, (table.shape[0], D // 2, 2),
+                   torch.float32),)
+    for _, t, shape, dtype in every:
+        if t is not None and (t.dtype is not dtype or t.shape != shape
+                              or t.get_device() != dev
+                              or not t.is_contiguous()):
+            break
+    else:
+        if dev >= 0 and k.is_contiguous():
+            return dev
+    for name, t, shape, dtype in every:
+        _expect(where, name, t, shape, dtype)
+    everything = (k, *(t for _, t, _, _ in every))
+    _same_device(where, *everything)
+    _need_cuda(*everything)
     return dev
 
 
@@ -741,24 +720,15 @@ def _kv8_call(name, call, dev, args):
         raise LwmError(st, name)
 
 
-def _on_stream(f):
-    """``stream=``: the call with that stream current, so that what it
-    allocates (results, workspace) belongs to the stream that uses it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
-
-
-@_on_stream
 def kv8_write(cache, k, v, positions, start, table, n_new=None,
-              rope_layout="interleaved"):
+              rope_layout="interleaved", stream=None):
     """Rotate and quantise k, v [B,T,H,D] bf16 into the cache at slots
     start[b] + t (in place; see the header for the block scales). ``n_new``
     [B]: new tokens of a padded row. Returns the cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_write(cache, k, v, positions, start, table, n_new,
+                             rope_layout)
     w = "kv8_write"
     B, H, L, D, code = _kv8_sizes(w, cache)
     _expect_dims(w, "k", k, 4)
@@ -766,8 +736,9 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None,
     new = (B, T, H, D)
     dev = _kv8_ready(
         w, cache, (B, H, L, D), table,
-        (("start", start), ("n_new", n_new)),
-        (("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
+        (("start", start, (B,), torch.int32),
+         ("n_new", n_new, (B,), torch.int32),
+         ("k", k, new, torch.bfloat16), ("v", v, new, torch.bfloat16),
          ("positions", positions, (B, T), torch.int32)))
     _kv8_call("lwm_kv8_write", lib().lwm_kv8_write, dev, (
         k.data_ptr(), v.data_ptr(), positions.data_ptr(), start.data_ptr(),
@@ -779,11 +750,13 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None,
     return cache
 
 
-@_on_stream
-def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None):
+def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     """Slots start[b] .. start[b] + T - 1 of the cache as (k_rot, v) bf16
     [B,T,H,D], zeros outside [0, min(kv_len[b], L)); the layout fwd_block
     takes rotated keys and values in."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_read(cache, start, T, kv_len, k_rot, v)
     w = "kv8_read"
     B, H, L, D, code = _kv8_sizes(w, cache)
     T = int(T)
@@ -791,8 +764,9 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None):
         raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
     shape = (B, T, H, D)
     dev = _kv8_ready(w, cache, (B, H, L, D), None,
-                     (("start", start), ("kv_len", kv_len)),
-                     (("k_rot", k_rot, shape, torch.bfloat16),
+                     (("start", start, (B,), torch.int32),
+                      ("kv_len", kv_len, (B,), torch.int32),
+                      ("k_rot", k_rot, shape, torch.bfloat16),
                       ("v", v, shape, torch.bfloat16)))
     if k_rot is None:
         k_rot = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
@@ -806,14 +780,18 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None):
     return k_rot, v
 
 
-@_on_stream
 def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
                n_recent=1, blocks=None, scores=None,
-               rope_layout="interleaved"):
+               rope_layout="interleaved", stream=None):
     """The ``n_select`` blocks of 128 slots per (row, cache head) whose key
     bounds admit the largest scores for q [B,Hq,D]: (blocks int32, scores
     fp32) [B,H,n_select], ascending, (-1, -inf) behind a short list. The
     first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_select(q, cache, kv_start, kv_len, q_pos, table,
+                              n_select, n_sink, n_recent, blocks, scores,
+                              rope_layout)
     w = "kv8_select"
     B, H, L, D, _ = _kv8_sizes(w, cache)
     Hq = _kv8_group(w, q, H)
@@ -823,8 +801,10 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     lists = (B, H, K)
     dev = _kv8_ready(
         w, cache, (B, H, L, D), table,
-        (("kv_start", kv_start), ("kv_len", kv_len), ("q_pos", q_pos)),
-        (("q", q, (B, Hq, D), torch.bfloat16),
+        (("kv_start", kv_start, (B,), torch.int32),
+         ("kv_len", kv_len, (B,), torch.int32),
+         ("q_pos", q_pos, (B,), torch.int32),
+         ("q", q, (B, Hq, D), torch.bfloat16),
          ("blocks", blocks, lists, torch.int32),
          ("scores", scores, lists, torch.float32)))
     if blocks is None:
@@ -845,14 +825,25 @@ def kv8_decode_workspace_size(B, L, Hq, H, n_blocks=None, D=HEAD_DIM) -> int:
         B, L, Hq, H, D, -1 if n_blocks is None else n_blocks))
 
 
-@_on_stream
+@functools.lru_cache(maxsize=1024)
+def _kv8_decode_bytes(dev, B, L, Hq, H, D, n_blocks):
+    """The workspace's size on a device, of the sizes alone."""
+    with torch.cuda.device(dev):
+        return max(1, int(lib().lwm_kv8_decode_workspace_size(
+            B, L, Hq, H, D, n_blocks)))
+
+
 def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
                out=None, lse=None, workspace=None,
-               rope_layout="interleaved"):
+               rope_layout="interleaved", stream=None):
     """One query token per (row, head), q [B,Hq,D], against slots
     [kv_start[b], kv_len[b]) of an 8-bit cache, or only those of ``blocks``
     [B,H,n] (a list of kv8_select, strictly ascending). Query head i reads
     cache head i // (Hq // H). Returns (out [B,Hq,D], lse [B,Hq])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv8_decode(q, cache, kv_start, kv_len, q_pos, table,
+                              blocks, out, lse, workspace, rope_layout)
     w = "kv8_decode"
     B, H, L, D, code = _kv8_sizes(w, cache)
     Hq = _kv8_group(w, q, H)
@@ -862,32 +853,30 @@ def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
         K = blocks.shape[2]
     dev = _kv8_ready(
         w, cache, (B, H, L, D), table,
-        (("kv_start", kv_start), ("kv_len", kv_len), ("q_pos", q_pos)),
-        (("q", q, (B, Hq, D), torch.bfloat16),
+        (("kv_start", kv_start, (B,), torch.int32),
+         ("kv_len", kv_len, (B,), torch.int32),
+         ("q_pos", q_pos, (B,), torch.int32),
+         ("q", q, (B, Hq, D), torch.bfloat16),
          ("blocks", blocks, (B, H, K), torch.int32),
          ("out", out, (B, Hq, D), torch.bfloat16),
          ("lse", lse, (B, Hq), torch.float32),
          ("workspace", workspace, getattr(workspace, "shape", None),
           getattr(workspace, "dtype", None))))
-    C = lib()
-    need = C.lwm_kv8_decode_workspace_size(B, L, Hq, H, D, K)
-    if workspace is None:
-        workspace = cache.k_bounds.new_empty(max(need, 1))     # int8: bytes
-    have = workspace.numel() * workspace.element_size()
-    if have < need:
-        raise LwmError(ERR_WORKSPACE, "workspace")
+    if workspace is None:                                      # int8: bytes
+        workspace = cache.k_bounds.new_empty(
+            _kv8_decode_bytes(dev, B, L, Hq, H, D, K))
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
         lse = cache.k_scale.new_empty((B, Hq))
-    _kv8_call("lwm_kv8_decode", C.lwm_kv8_decode, dev, (
+    _kv8_call("lwm_kv8_decode", lib().lwm_kv8_decode, dev, (
         q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
         kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
         None if blocks is None else blocks.data_ptr(), K, table.data_ptr(),
         table.shape[0], B, L, Hq, H, D, DTYPE_BF16, code,
         _layout_code(rope_layout), out.data_ptr(), lse.data_ptr(),
-        workspace.data_ptr(), have))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return out, lse
 
 

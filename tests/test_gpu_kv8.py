@@ -747,3 +747,20 @@ def test_offsets_past_32_bits(cuda_dev):
     assert abs(float(lse[0, h]) - (s.max() + np.log(p.sum()))) <= 2 ** -6
     o = p @ val(vr[0, :, h]) / p.sum()
     assert np.abs(val(out[0, h]) - o).max() <= 2 ** -5
+
+
+def test_a_small_workspace_is_refused(cuda_dev):
+    c = filled(2, 640, 2, "e4m3")
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    table = ops.rope_table(THETA, 64)
+    need = ops.kv8_decode_workspace_size(2, 640, 4, 2)
+    assert need > 0
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device="cuda")
+    for at, size in ((0, need - 1), (8, need)):       # too short, misaligned
+        ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+        with pytest.raises(ops.LwmError):
+            ops.kv8_decode(q, c, i32([0, 0]), i32([640, 5]), i32([1, 2]),
+                           table, out=out, lse=lse,
+                           workspace=ws[at:at + size])
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
