@@ -262,11 +262,14 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
 // read once and each code written once. K keeps the channels' smallest and
 // largest value, which give the block's maximum as well as its bounds. One
 // barrier of the group per box.
-// The traffic alone takes 124 us for 32K tokens x 32 heads (805 MB at the
-// rate of a copy); this takes 148, the same without the rotation or the
-// ranges. All K before V took 153, shares of whole runs of heads 164 for the
-// same tokens in 32 rows, one group of 16 warps 187, and a CTA per block and
-// head without TMA 536.
+// 32K tokens x 32 heads (805 MB) take 148 us. The traffic alone would take
+// 115 to 124 (an elementwise stream, a copy), the warps' work on boxes that
+// come from L2 and go nowhere 114; the two overlap in part. (V in K's place
+// takes 120, K without its rotation 148: it is the chain from the box to its
+// maximum and on to the codes that counts, not the arithmetic; 64-bit stores
+// 144 to 149.) All K before V took 153, shares of whole runs of heads 164
+// for the same tokens in 32 rows, one group of 16 warps 187, and a CTA per
+// block and head without TMA 536.
 constexpr int kWrGroups = 2;
 constexpr int kWrGroup = 256;                       // threads of a group
 constexpr int kWrWarps = kWrGroup / 32;
