@@ -254,26 +254,27 @@ kv8_write_few_kernel(const __grid_constant__ Kv8WriteArgs a, int64_t items) {
 // The heads' [128 tokens][128] bf16 boxes, K and V, come in by TMA through a
 // ring of stages, the angles of a block's tokens (512 bytes each) by bulk
 // copies while the last V boxes of the block before are worked on. Two
-// groups of eight warps take the boxes in turn; K and V alternate within
-// each group, so that the instructions of the one and the traffic of the
-// other even out. 16 lanes share a token, eight channels each (4c .. 4c + 3
+// groups of eight warps take the boxes in turn, each with a loader and
+// stages of its own, so that neither waits for the other; K and V alternate
+// within each group, so that the instructions of the one and the traffic of
+// the other even out. 16 lanes share a token, eight channels each (4c .. 4c + 3
 // and the same 64 further up), eight tokens per thread; the rotated block
 // stays in registers between the maximum and the encoding, so each input is
 // read once and each code written once. K keeps the channels' smallest and
 // largest value, which give the block's maximum as well as its bounds. One
 // barrier of the group per box.
-// 32K tokens x 32 heads (805 MB) take 148 us. The traffic alone would take
+// 32K tokens x 32 heads (805 MB) take 145 us. The traffic alone would take
 // 115 to 124 (an elementwise stream, a copy), the warps' work on boxes that
-// come from L2 and go nowhere 114; the two overlap in part. (V in K's place
-// takes 120, K without its rotation 148: it is the chain from the box to its
-// maximum and on to the codes that counts, not the arithmetic; 64-bit stores
-// 144 to 149.) All K before V took 153, shares of whole runs of heads 164
-// for the same tokens in 32 rows, one group of 16 warps 187, and a CTA per
-// block and head without TMA 536.
+// come from L2 and go nowhere 114; the two overlap in part. One loader for
+// both groups took 148 (147 without the rotation, 120 with V boxes in K's
+// place: it is the chain from the box to its maximum and on to the codes
+// that counts, not the arithmetic), all K before V 153, shares of whole runs
+// of heads 164 for the same tokens in 32 rows, one group of 16 warps 187,
+// and a CTA per block and head without TMA 536.
 constexpr int kWrGroups = 2;
 constexpr int kWrGroup = 256;                       // threads of a group
 constexpr int kWrWarps = kWrGroup / 32;
-constexpr int kWrThreads = kWrGroups * kWrGroup + 32;  // and the loader's
+constexpr int kWrThreads = kWrGroups * (kWrGroup + 32);  // and the loaders'
 constexpr int kWrLanes = 16;
 constexpr int kWrStep = kWrGroup / kWrLanes;        // tokens per pass
 constexpr int kWrPasses = kKv8Block / kWrStep;
@@ -287,10 +288,18 @@ struct __align__(16) WriteBox {
   int64_t codes;      // first code of the block
   int64_t at;         // its scale
   int lo, hi;         // its new slots
-  int flags;          // kBoxKey, kBoxEnd
+  int flags;
   int item;           // counts the CTA's blocks (angles)
 };
-enum : int { kBoxKey = 1, kBoxEnd = 2 };
+enum : int {
+  kBoxKey = 1,
+  kBoxEnd = 2,
+  // Of every run of heads, each group waits for the angles, so that it never
+  // is a run ahead of them, and says once that it needs them no more: at its
+  // K boxes and the last of them, or at its V box where it has no K.
+  kBoxAngles = 4,
+  kBoxFree = 8,
+};
 
 // shared memory (bytes): stages, angles, channel ranges
 // [group][box parity][lo, hi][warp][128], maxima [group][parity][warp],
@@ -302,7 +311,7 @@ constexpr int kWrMax = kWrChan + kWrGroups * 2 * kWrChanHalf;
 constexpr int kWrBox = kWrMax + kWrGroups * 2 * kWrWarps * 4;
 constexpr int kWrBars = kWrBox + kWrStages * int(sizeof(WriteBox));
 constexpr int wFull = 0, wEmpty = kWrStages, wAngles = 2 * kWrStages,
-              kWrNumBars = wAngles + 1;
+              wFree = wAngles + 1, kWrNumBars = wFree + 1;
 constexpr int kWrSmem = kWrBars + kWrNumBars * 8 + 16 + 128;
 static_assert(kWrSmem <= 232448, "shared memory per CTA");
 
@@ -387,8 +396,11 @@ __device__ __forceinline__ bool write_box(const Kv8WriteArgs& a,
   float amax = 0.f;
   // the warp has read the box and its angles
   __syncwarp();
-  if (lane == 0)
-    mbar_arrive(smem_u32(w.smem) + kWrBars + 8u * (wEmpty + w.stage));
+  if (lane == 0) {
+    const uint32_t bars = smem_u32(w.smem) + kWrBars;
+    mbar_arrive(bars + 8u * (wEmpty + w.stage));
+    if (box.flags & kBoxFree) mbar_arrive(bars + 8u * wFree);
+  }
   if (kKey) {
     // lanes 0-15 keep the smallest values of the warp's two tokens of each
     // pass, the others the largest
@@ -549,7 +561,9 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWrNumBars; ++i)
-      mbar_init(bar(i), i >= wEmpty && i < wEmpty + kWrStages ? kWrWarps : 1);
+      mbar_init(bar(i), i >= wEmpty && i < wEmpty + kWrStages ? kWrWarps
+                        : i == wFree ? kWrGroups * kWrWarps
+                                     : 1);
     fence_mbar_init();
     *abort_word = 0;
   }
@@ -558,9 +572,13 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
   pdl_trigger();
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
 
-  if (warp == kWrGroups * kWrWarps) {
-    // -------------------------------------------------------------- loader
-    int n = 0, item = 0, last_key = -1;
+  if (warp >= kWrGroups * kWrWarps) {
+    // -------------------------------------------- loaders, one per group
+    // n counts the boxes of both groups, which take turns; each group has
+    // every other stage. The first loader also fetches the angles.
+    const int own = warp - kWrGroups * kWrWarps;
+    static_assert(kWrGroups == 2 && kWrStages % 2 == 0, "a group's own stages");
+    int n = 0, item = 0, angles = 0;
     bool ok = true;
     // rows 32 at a time, one per lane: its new slots, its blocks and those
     // of the rows up to it, `before` those of the rows below row0
@@ -614,56 +632,66 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int lo = int(max(ns.lo - base, int64_t(0)));
       const int hi = int(min(ns.hi - base, int64_t(kKv8Block)));
       const int64_t tok = base - ns.start;   // of the block's first slot
-      // the angles before are free once their last K boxes are read
-      for (int m = max(0, n - kWrStages); ok && m <= last_key; ++m)
-        ok = wait(wEmpty + m % kWrStages, m / kWrStages);
-      if (!ok) break;
-      // consecutive positions are consecutive rows of the table: one copy;
-      // one per token (a quarter of the loader's time) only where they jump
-      int p[kKv8Block / 32];
-      const int32_t* pos = a.positions + int64_t(b) * a.T + tok;
+      if (own == 0) {
+        if (item > 0) ok = wait(wFree, item - 1);
+        if (!ok) break;
+        // consecutive positions are consecutive rows of the table: one copy;
+        // one per token (a quarter of the loader's time) only where they jump
+        int p[kKv8Block / 32];
+        const int32_t* pos = a.positions + int64_t(b) * a.T + tok;
 #pragma unroll
-      for (int k = 0; k < kKv8Block / 32; ++k) {
-        const int r = lane + 32 * k;
-        p[k] = r >= lo && r < hi
-                   ? max(0, min(ld_now(pos + r), a.max_pos - 1))
-                   : -1;
-      }
-      const int first =
-          max(0, min(ld_now(pos + lo), a.max_pos - 1)) - lo;   // of slot 0
-      bool run = true;
-#pragma unroll
-      for (int k = 0; k < kKv8Block / 32; ++k)
-        run = run && (p[k] < 0 || p[k] == first + lane + 32 * k);
-      run = __all_sync(0xffffffffu, run);
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar(wAngles), (hi - lo) * (kHeadDim * 4));
-      __syncwarp();
-      if (run) {
-        if (lane == 0)
-          bulk_load(sbase + kWrAng + lo * (kHeadDim * 4),
-                    a.table + int64_t(first + lo) * kHeadDim,
-                    (hi - lo) * (kHeadDim * 4), bar(wAngles));
-      } else {
+        for (int k = 0; k < kKv8Block / 32; ++k) {
+          const int r = lane + 32 * k;
+          p[k] = r >= lo && r < hi
+                     ? max(0, min(ld_now(pos + r), a.max_pos - 1))
+                     : -1;
+        }
+        const int first =
+            max(0, min(ld_now(pos + lo), a.max_pos - 1)) - lo;   // of slot 0
+        bool run = true;
 #pragma unroll
         for (int k = 0; k < kKv8Block / 32; ++k)
-          if (p[k] >= 0)
-            bulk_load(sbase + kWrAng + (lane + 32 * k) * (kHeadDim * 4),
-                      a.table + int64_t(p[k]) * kHeadDim, kHeadDim * 4,
-                      bar(wAngles));
-      }
-      for (int i = 0; i < 2 * heads; ++i, ++n) {
-        // K 0, K 1; V 0, K 2; K 3, V 1; V 2, K 4; ... V n - 2, V n - 1
-        bool key = i < min(2, heads);
-        int h = i;
-        if (!key) {
-          const int pair = (i >> 1) - 1;
-          key = pair < heads - 2 && ((i ^ pair) & 1) != 0;
-          h = pair >= heads - 2 ? i - heads : key ? pair + 2 : pair;
+          run = run && (p[k] < 0 || p[k] == first + lane + 32 * k);
+        run = __all_sync(0xffffffffu, run);
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar(wAngles), (hi - lo) * (kHeadDim * 4));
+        __syncwarp();
+        if (run) {
+          if (lane == 0)
+            bulk_load(sbase + kWrAng + lo * (kHeadDim * 4),
+                      a.table + int64_t(first + lo) * kHeadDim,
+                      (hi - lo) * (kHeadDim * 4), bar(wAngles));
+        } else {
+#pragma unroll
+          for (int k = 0; k < kKv8Block / 32; ++k)
+            if (p[k] >= 0)
+              bulk_load(sbase + kWrAng + (lane + 32 * k) * (kHeadDim * 4),
+                        a.table + int64_t(p[k]) * kHeadDim, kHeadDim * 4,
+                        bar(wAngles));
         }
-        h += h0;
-        const int s = n % kWrStages;
-        if (n >= kWrStages) ok = wait(wEmpty + s, n / kWrStages - 1);
+        ++angles;
+      }
+      // K 0, K 1; V 0, K 2; K 3, V 1; V 2, K 4; ... V m - 2, V m - 1
+      auto head_of = [&](int i, bool& key) {
+        key = i < min(2, heads);
+        if (key) return i;
+        const int pair = (i >> 1) - 1;
+        key = pair < heads - 2 && ((i ^ pair) & 1) != 0;
+        return pair >= heads - 2 ? i - heads : key ? pair + 2 : pair;
+      };
+      // the group's last K, or its one V
+      int last = 2 * heads - 2 + own;
+      for (bool key = false; last > own; last -= 2) {
+        head_of(last, key);
+        if (key) break;
+      }
+      int i = own;
+      for (; i < 2 * heads; i += 2) {
+        bool key;
+        const int h = h0 + head_of(i, key);
+        const int at = n + i;
+        const int s = at % kWrStages;
+        if (at >= kWrStages) ok = wait(wEmpty + s, at / kWrStages - 1);
         if (!ok) break;
         if (lane == 0) {
           const int64_t bh = int64_t(b) * a.H + h;
@@ -672,7 +700,9 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
           x.at = bh * nblk + base / kKv8Block;
           x.lo = lo;
           x.hi = hi;
-          x.flags = key ? kBoxKey : 0;
+          x.flags = (key ? kBoxKey : 0) |
+                    (key || i == last ? kBoxAngles : 0) |
+                    (i == last ? kBoxFree : 0);
           x.item = item;
           boxes[s] = x;
           mbar_arrive_expect_tx(bar(wFull + s), kWrTile);
@@ -681,28 +711,30 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
                       bar(wFull + s), 0, h, int(tok), b);
         }
         __syncwarp();
-        if (key) last_key = n;
       }
+      n += ok ? 2 * heads : i - own;
       ++item;
     }
-    // one end for each group, behind all boxes
-    const int loads = n;
-    for (int g = 0; ok && g < kWrGroups; ++g, ++n) {
-      const int s = n % kWrStages;
-      if (n >= kWrStages) ok = wait(wEmpty + s, n / kWrStages - 1);
+    // the end, behind the group's boxes
+    const int end = n + own;
+    const bool ended = ok;
+    if (ok) {
+      const int s = end % kWrStages;
+      if (end >= kWrStages) ok = wait(wEmpty + s, end / kWrStages - 1);
       if (ok && lane == 0) {
         boxes[s].flags = kBoxEnd;
         mbar_arrive(bar(wFull + s));
       }
       __syncwarp();
     }
-    // no load is in flight when the CTA leaves, abandoned or not (a stage
+    // no load is in flight when the CTA leaves, abandoned or not (the stage
     // that an end has taken was empty before)
-    for (int m = max(0, n - kWrStages); m < loads; ++m)
+    for (int m = max(own, ended && ok ? end - 2 : end - kWrStages); m < end;
+         m += 2)
       mbar_wait(bar(wFull + m % kWrStages), (m / kWrStages) & 1, nullptr,
                 status, kWrWaitNs);
-    if (item > 0)
-      mbar_wait(bar(wAngles), (item - 1) & 1, nullptr, status, kWrWaitNs);
+    if (angles > 0)
+      mbar_wait(bar(wAngles), (angles - 1) & 1, nullptr, status, kWrWaitNs);
     return;
   }
 
@@ -715,7 +747,7 @@ kv8_write_kernel(const __grid_constant__ CUtensorMap tm_k,
     bool ok = __all_sync(0xffffffffu, wait(wFull + s, n / kWrStages));
     const WriteBox box = boxes[s];
     if (ok) ok = !(box.flags & kBoxEnd);
-    if (ok && (box.flags & kBoxKey))
+    if (ok && (box.flags & kBoxAngles))
       ok = __all_sync(0xffffffffu, wait(wAngles, box.item));
     if (!ok) {
       group_all(1 + group, false);
