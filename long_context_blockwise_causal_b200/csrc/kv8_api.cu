@@ -25,7 +25,9 @@ bool words_ok(std::initializer_list<const void*> ps) {
   return aligned_to(ps, 4);
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? LWM_OK : LWM_ERR_CUDA; }
+int cuda_status(cudaError_t e) {
+  return e == cudaSuccess ? LWM_OK : LWM_ERR_CUDA;
+}
 
 // Slots or tokens of all rows are counted in 32 bits, rounded up to blocks.
 constexpr int64_t kMostSlots = (int64_t(1) << 31) - kKv8Block;
@@ -213,7 +215,8 @@ int lwm_kv8_decode(const void* q, const void* k_cache, const void* v_cache,
   if (s != LWM_OK) return s;
   const bool listed = n_blocks >= 0;
   // tiles (blocks of all rows and heads) are counted in 32 bits
-  const int64_t per = listed ? n_blocks : (int64_t(L) + kKv8Block - 1) / kKv8Block;
+  const int64_t per =
+      listed ? n_blocks : (int64_t(L) + kKv8Block - 1) / kKv8Block;
   if (int64_t(B) * H * per >= (int64_t(1) << 31) - 4096)
     return LWM_ERR_UNSUPPORTED;
   if (dtype != LWM_DTYPE_BF16) return LWM_ERR_UNSUPPORTED;

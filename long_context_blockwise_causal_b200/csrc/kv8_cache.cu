@@ -432,7 +432,8 @@ __device__ __forceinline__ bool write_box(const Kv8WriteArgs& a,
       const float got = __shfl_xor_sync(0xffffffffu, low ? mx : mn, 16);
       m[j] = low ? min_nan(mn, got) : max_nan(mx, got);
     }
-    float* to = w.chan(w.parity) + (low ? wg : kWrWarps + wg) * kHeadDim + 4 * c;
+    float* to =
+        w.chan(w.parity) + (low ? wg : kWrWarps + wg) * kHeadDim + 4 * c;
     *reinterpret_cast<float4*>(to) = make_float4(m[0], m[1], m[2], m[3]);
     *reinterpret_cast<float4*>(to + 64) =
         make_float4(m[4], m[5], m[6], m[7]);
@@ -534,7 +535,7 @@ __device__ __forceinline__ bool write_box(const Kv8WriteArgs& a,
     }
     int bound = upper ? bound_hi<kInt8>(code) : bound_lo<kInt8>(code);
     int8_t* bd = a.k_bounds + box.at * 2 * kHeadDim + t;
-    if (!kFull && box.lo > 0 && !grew)     // the older tokens' bounds still hold
+    if (!kFull && box.lo > 0 && !grew)   // the older tokens' bounds still hold
       bound = upper ? max(bound, int(*bd)) : min(bound, int(*bd));
     *bd = int8_t(bound);
   }

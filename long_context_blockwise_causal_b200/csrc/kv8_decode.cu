@@ -457,6 +457,9 @@ struct Walker {
   // current (row, head): tiles [j, je) are left
   int h, j, je, seg_flags;
   bool emitted;
+  // of a listed call: entry j of the list, fetched ahead, and the one before
+  const int32_t* list;
+  int entry, left;
 
   __device__ __forceinline__ void open() {   // at tile u < u1
     while (u >= row_at + rt.n * rows.H) {
@@ -474,6 +477,11 @@ struct Walker {
     seg_flags = (p0 >= u0 && p1 <= u1 ? kWhole : 0) | (p0 < u0 ? 0 : kSlot1);
     emitted = false;
     u += je - j;
+    if (rows.listed) {
+      list = blocks + (int64_t(b) * rows.H + h) * rows.K;
+      entry = ld_now(list + j);
+      left = j > 0 ? ld_now(list + j - 1) : -1;
+    }
   }
   // False at the end of the CTA's share.
   __device__ __forceinline__ bool next(Tile& t) {
@@ -493,11 +501,10 @@ struct Walker {
       int blk = rt.t0 + j;
       bool ok = true;
       if (rows.listed) {
-        const int32_t* list =
-            blocks + (int64_t(b) * rows.H + h) * rows.K;
-        blk = ld_now(list + j);
-        ok = blk >= rt.t0 && int64_t(blk) * kKv8Block < rt.len &&
-             (j == 0 || blk > ld_now(list + j - 1));
+        blk = entry;
+        if (j + 1 < je) entry = ld_now(list + j + 1);
+        ok = blk >= rt.t0 && int64_t(blk) * kKv8Block < rt.len && blk > left;
+        left = blk;
       }
       ++j;
       if (!ok) continue;
@@ -1167,7 +1174,8 @@ int kv8_decode_grid(int B, int L, int H, int G, int K) {
       G > 8 ? Dec<false, 16>::kPerSm : Dec<false, 8>::kPerSm;
   const int64_t per = K >= 0 ? K : (L + kKv8Block - 1) / kKv8Block;
   const int64_t most = int64_t(B) * H * per;
-  return int(std::max<int64_t>(1, std::min<int64_t>(most, per_sm * sm_count())));
+  return int(
+      std::max<int64_t>(1, std::min<int64_t>(most, per_sm * sm_count())));
 }
 
 size_t kv8_part_floats(int B, int L, int H, int G, int K) {
