@@ -764,3 +764,43 @@ def test_a_small_workspace_is_refused(cuda_dev):
                            workspace=ws[at:at + size])
     torch.cuda.synchronize()
     assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+def test_two_streams_at_once(cuda_dev):
+    """Prompts written, blocks chosen and tokens decoded on two streams at
+    the same time, each with its cache, give what they give alone."""
+    B, H, G, L, T = 3, 8, 2, 4000, 3000
+    kinds = ("e4m3", "int8")
+    made = []
+    for i, kind in enumerate(kinds):
+        k, v = tokens(B, T, H, 50 + i)
+        q, pos, table = queries(B, H * G, L, 60 + i)
+        made.append((kind, k, v, q, pos, table))
+    at = i32([0, 77, 900])
+    n, z = at + T, i32([0, 0, 0])
+    where = torch.arange(T, dtype=torch.int32, device="cuda").expand(B, T)
+    where = where.contiguous()
+
+    def run(kind, k, v, q, pos, table):
+        c = ops.kv8_cache(B, L, H, dtype=DT[kind])
+        ops.kv8_write(c, k, v, where, at, table)
+        bl, sc = ops.kv8_select(q, c, z, n, pos, table, 6)
+        return [*c, bl, sc, *ops.kv8_decode(q, c, z, n, pos, table),
+                *ops.kv8_decode(q, c, z, n, pos, table, blocks=bl)]
+
+    alone = [run(*m) for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in kinds]
+    for _ in range(4):
+        got = []
+        for st, m in zip(streams, made):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(run(*m))
+        torch.cuda.synchronize()
+        assert ops.last_status() == ops.OK
+        for a, b in zip(alone, got):
+            for x, y in zip(a, b):
+                x, y = ((t.view(torch.int8) if t.dtype.itemsize == 1 else t)
+                        for t in (x, y))
+                assert torch.equal(x, y)
