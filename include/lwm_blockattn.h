@@ -524,8 +524,12 @@ LWM_API size_t lwm_kv8_decode_workspace_size(int B, int L, int Hq, int H,
  *   out [B][Hq][D] bf16; lse [B][Hq] fp32 natural log over the slots read
  *   (-inf, with out = 0, where there is none).
  * Slots outside the range are never used, whatever they hold. Scores, the
- * softmax and the sums are fp32. Async on stream; bounded waits report to
- * lwm_blockattn_last_status. */
+ * softmax's maximum and sum, and the sums of both products are fp32. The
+ * products take the cache's codes as they are against sums of codes for the
+ * rotated query (e4m3: to 2^-20 of each channel; int8: to 2^-22 of the
+ * largest) and for the softmax weights (e4m3: to 2^-16 of each weight, 2^-21
+ * on average; int8: to 2^-24 of the largest of a block). Async on stream;
+ * bounded waits report to lwm_blockattn_last_status. */
 LWM_API int lwm_kv8_decode(const void* q, const void* k_cache,
                            const void* v_cache, const float* k_scale,
                            const float* v_scale, const int32_t* kv_start,

@@ -142,17 +142,20 @@ __host__ __device__ constexpr int part_stride(int G) {
 // codes (terms), each carrying what the ones before it left, and each term
 // of each head is one column n; products of codes are exact and the columns
 // are added up in fp32. e4m3: terms 1/16 apart, 5 for q (2^-20 of a channel,
-// or 2^-34 of the largest), 3 for p (2^-12 of a weight, or 2^-26 of the
-// largest). int8: terms 1/254 apart, 3 for q (2^-22 of the largest channel)
-// and 3 for p (2^-24 of the largest weight). Weights are taken against the
-// tile's own maximum, so what the terms cannot hold is small against the
-// tile's own sum, however far the running maximum lies above it.
+// or 2^-34 of the largest), 4 for p (2^-16 of a weight at most, 2^-21 on
+// average, or 2^-30 of the largest). int8: terms 1/254 apart, 3 for q (2^-22
+// of the largest channel) and 3 for p (2^-24 of the largest weight). Weights
+// are taken against the tile's own maximum, so what the terms cannot hold is
+// small against the tile's own sum, however far the running maximum lies
+// above it. With these terms out is off by less than fp32 sums in another
+// order are (2-norm of 2048 slots, before rounding: 3e-7); three terms for
+// an e4m3 weight left 1.4e-5, which turned roundings of out to bf16.
 //
 // Softmax warps: four per group of at most 8 heads; thread t of a group is
 // slot t of S (scores, maximum, weights) and channel t of O (accumulator).
 // The warp after them issues the products, the last one walks the tiles and
 // loads them by TMA. The products of one tile run while the softmax works
-// on the next: S, P and O are double buffered.
+// on the next: S, P and, up to 8 heads, O are double buffered.
 //
 // Bound by HBM (256 bytes per slot and cache head) up to 8 query heads per
 // cache head: a 1M-slot cache of 32 heads in 1.16 ms (7.4 TB/s), 16 rows x
@@ -186,10 +189,13 @@ struct Dec {
   static constexpr int kThreads = 128 * kGroups + 64;
   static constexpr int kPerSm = 2;                      // CTAs
   static constexpr int kQTerms = kInt8 ? 3 : 5;
-  static constexpr int kPTerms = 3;
+  static constexpr int kPTerms = kInt8 ? 3 : 4;
   static constexpr int kNq = (kQTerms * GP + 15) / 16 * 16;
   static constexpr int kNp = (kPTerms * GP + 15) / 16 * 16;
-  static constexpr int kCols = 2 * kNq + 2 * kNp;
+  // O is double buffered where the columns allow: 16 heads of e4m3 have one,
+  // which is read before the next tile's weights are handed over
+  static constexpr int kOBufs = 2 * kNq + 2 * kNp <= 256 ? 2 : 1;
+  static constexpr int kCols = 2 * kNq + kOBufs * kNp;
   static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static_assert(kCols <= 256, "CTAs share the SM's 512 columns");
   // factor of the first term
@@ -681,7 +687,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
               sdesc_sw128(sbase + C::kP + (i & 1) * C::kPBytes, 16, 1024);
 #pragma unroll
           for (int k = 0; k < kKv8Block / 32; ++k)
-            mma8<kInt8>(tmem + 2 * C::kNq + (i & 1) * C::kNp,
+            mma8<kInt8>(tmem + 2 * C::kNq + i % C::kOBufs * C::kNp,
                         vd + uint64_t(k * (32 * kHeadDim >> 4)), pd + 2 * k,
                         idp, k > 0);
         }
@@ -814,7 +820,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (!live) return;
       tc_fence_after();
       uint32_t r[C::kPTerms][GH];
-      const uint32_t at = my_tmem + 2 * C::kNq + (i & 1) * C::kNp;
+      const uint32_t at = my_tmem + 2 * C::kNq + i % C::kOBufs * C::kNp;
 #pragma unroll
       for (int n = 0; n < C::kPTerms; ++n) tmem_ld<GH>(at + n * GP, r[n]);
       float al[GH], be[GH];
@@ -923,6 +929,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         fence_proxy_async_smem();
       }
+      // the product of the tile before ran meanwhile; where there is one O,
+      // it is read before these weights let the next product write it
+      if (C::kOBufs == 1 && pending) add_o(i - 1, true);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::bP + (i & 1)));
       // the next (row, head)'s query
@@ -930,8 +939,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (C::kGroups > 1) fetch_q(nxt);
         make_q((seg + 1) & 1);
       }
-      // the product of the tile before ran meanwhile
-      if (pending) add_o(i - 1, true);
+      if (C::kOBufs == 2 && pending) add_o(i - 1, true);
       pending = live;
       if (cur.flags & kLast) {
         add_o(i, live);
