@@ -383,18 +383,20 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Lets `Kernel` use `bytes` of dynamic shared memory on the current device;
-// asks the runtime once per kernel and device.
-template <auto Kernel>
-inline cudaError_t allow_smem(int bytes) {
-  static std::atomic<int> allowed[kKnownDevices];
+// Lets `Kernel` use up to `Bytes` of dynamic shared memory on the current
+// device; asks the runtime once per kernel and device. One size per kernel,
+// the most that any launch of it takes: threads that ask at the same time then
+// ask for the same, and the order in which they do does not matter.
+template <auto Kernel, int Bytes>
+inline cudaError_t allow_smem() {
+  static std::atomic<bool> allowed[kKnownDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < kKnownDevices && allowed[dev].load() >= bytes) return cudaSuccess;
+  if (dev < kKnownDevices && allowed[dev].load()) return cudaSuccess;
   e = cudaFuncSetAttribute(
-      Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < kKnownDevices) allowed[dev].store(bytes);
+      Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Bytes);
+  if (e == cudaSuccess && dev < kKnownDevices) allowed[dev].store(true);
   return e;
 }
 

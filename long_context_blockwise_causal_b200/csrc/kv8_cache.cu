@@ -834,7 +834,8 @@ cudaError_t launch_many(const Kv8WriteArgs& a, int* status, cudaStream_t st) {
   if (!make_tokens_map(&mk, a.x[0], a.B, a.T, a.H) ||
       !make_tokens_map(&mv, a.x[1], a.B, a.T, a.H))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<kv8_write_kernel<kInt8, kHalf>>(kWrSmem);
+  const cudaError_t e =
+      allow_smem<kv8_write_kernel<kInt8, kHalf>, kWrSmem>();
   if (e != cudaSuccess) return e;
   // never more CTAs than there can be (block, head) pairs
   const int64_t pairs =

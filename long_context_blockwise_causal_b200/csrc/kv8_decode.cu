@@ -1203,7 +1203,7 @@ cudaError_t launch_tiles(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
   if (!make_codes_map(&mk, k, int64_t(a.B) * a.H, L) ||
       !make_codes_map(&mv, v, int64_t(a.B) * a.H, L))
     return cudaErrorInvalidValue;
-  const cudaError_t e = allow_smem<kv8_decode_kernel<kInt8, GP>>(D::kSmem);
+  const cudaError_t e = allow_smem<kv8_decode_kernel<kInt8, GP>, D::kSmem>();
   if (e != cudaSuccess) return e;
   return launch_dependent(kv8_decode_kernel<kInt8, GP>, dim3(C),
                           dim3(D::kThreads), D::kSmem, st, mk, mv, a);

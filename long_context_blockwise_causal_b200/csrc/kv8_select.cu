@@ -20,7 +20,9 @@ namespace {
 constexpr int kSelPasses = 3;                // digits of up to 11 bits
 constexpr int kSelBins = 2048;
 constexpr int kSelMost = 8;                  // CTAs per cluster
-static_assert(kKv8SelectMaxLen / kKv8Block * 4 <= 160 * 1024,
+// bytes of the scores of the longest row
+constexpr int kSelMostSmem = kKv8SelectMaxLen / kKv8Block * 4;
+static_assert(kSelMostSmem <= 160 * 1024,
               "a row's scores fit one CTA's shared memory");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -457,7 +459,8 @@ cudaError_t launch_rows(const Kv8SelectArgs& a, int C, cudaStream_t st) {
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
   const int64_t grid = int64_t(a.B) * a.H * C;
   const size_t smem = size_t(nblk + 3) / 4 * 16;
-  cudaError_t e = allow_smem<kv8_select_kernel<GP, Threads>>(int(smem));
+  const cudaError_t e =
+      allow_smem<kv8_select_kernel<GP, Threads>, kSelMostSmem>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
