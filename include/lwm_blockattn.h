@@ -479,7 +479,9 @@ LWM_API int lwm_kv8_write(const void* k, const void* v,
                           float* v_scale, int8_t* k_bounds, void* stream);
 
 /* Reads slots back: k_rot, v [B][T][H][D] bf16, the layout
- * lwm_blockattn_fwd_block takes keys and values in. Token t of row b is
+ * lwm_blockattn_fwd_block takes keys and values in. That call reads as many
+ * key heads as q has: with grouped query heads (Hq > H) the caller repeats
+ * each head Hq / H times first. Token t of row b is
  * slot start[b] + t; a slot outside [0, min(kv_len[b], L)) reads as zeros
  * (kv_len NULL: L). Async on stream. */
 LWM_API int lwm_kv8_read(const void* k_cache, const void* v_cache,

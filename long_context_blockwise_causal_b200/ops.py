@@ -335,10 +335,26 @@ def fwd_block(q, k_rot, v, seg_q, pos_q, seg_k, q_off, k_off, theta,
     """Partial forward of query rows [q_off, q_off+Nq) against the rotated
     key / value rows [k_off, k_off+Nk) of the same packed sequence (one step
     of a ring). Returns (out [B,Nq,H,D] bf16, lse [B,H,Nq] fp32); rows that
-    see no key get (0, -inf)."""
-    _need_cuda(q, k_rot, v, seg_q, pos_q, seg_k, out, lse, workspace, table)
+    see no key get (0, -inf). k_rot and v have q's heads: those of a grouped
+    cache are repeated by the caller."""
+    w = "fwd_block"
+    _expect_dims(w, "q", q, 4)
+    _expect_dims(w, "k_rot", k_rot, 4)
     B, Nq, H, D = q.shape
     Nk = k_rot.shape[1]
+    for name, t, shape in (("q", q, q.shape), ("k_rot", k_rot, (B, Nk, H, D)),
+                           ("v", v, (B, Nk, H, D)), ("out", out, q.shape)):
+        _expect(w, name, t, shape, torch.bfloat16)
+    for name, t, shape in (("seg_q", seg_q, (B, Nq)), ("pos_q", pos_q, (B, Nq)),
+                           ("seg_k", seg_k, (B, Nk))):
+        _expect(w, name, t, shape, torch.int32)
+    _expect(w, "lse", lse, (B, H, Nq), torch.float32)
+    if table is not None:
+        _expect_dims(w, "table", table, 3)
+        _expect(w, "table", table, (table.shape[0], D // 2, 2), torch.float32)
+    _same_device(w, q, k_rot, v, seg_q, pos_q, seg_k, out, lse, workspace,
+                 table)
+    _need_cuda(q, k_rot, v, seg_q, pos_q, seg_k, out, lse, workspace, table)
     if table is not None and table.shape[0] < max_pos:
         raise ValueError("rope table shorter than max_pos")
     if out is None:
@@ -753,7 +769,10 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None,
 def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     """Slots start[b] .. start[b] + T - 1 of the cache as (k_rot, v) bf16
     [B,T,H,D], zeros outside [0, min(kv_len[b], L)); the layout fwd_block
-    takes rotated keys and values in."""
+    takes rotated keys and values in, where the queries have as many heads as
+    the cache. Those of a grouped cache are repeated first, head i of the
+    queries being given head i // (Hq // H):
+    ``k_rot.repeat_interleave(Hq // H, 2)``."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv8_read(cache, start, T, kv_len, k_rot, v)
