@@ -1131,10 +1131,11 @@ kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
   // rows that see nothing
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (row_tiles(rows, b).n > 0) continue;
-    const int64_t q0 = int64_t(b) * a.H * a.G;
-    for (int i = t; i < a.H * a.G * (kHeadDim / 2); i += kJoinThreads)
+    // (a row's query heads fit 32 bits, its channels need not)
+    const int64_t heads = int64_t(a.H) * a.G, q0 = b * heads;
+    for (int64_t i = t; i < heads * (kHeadDim / 2); i += kJoinThreads)
       reinterpret_cast<uint32_t*>(a.out)[q0 * (kHeadDim / 2) + i] = 0u;
-    for (int i = t; i < a.H * a.G; i += kJoinThreads)
+    for (int64_t i = t; i < heads; i += kJoinThreads)
       a.lse[q0 + i] = -INFINITY;
   }
   // a call of one CTA has no cut; and there may be no tiles behind one
