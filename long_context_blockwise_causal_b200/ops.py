@@ -677,6 +677,15 @@ def _kv8_sizes(where, cache):
     return B, H, L, D, code
 
 
+def _kv8_count(where, name, n, least):
+    """n as a whole number from `least` to the largest C int (ctypes would
+    pass on the low 32 bits of a larger one)."""
+    n = int(n)
+    if not least <= n < 1 << 31:
+        raise LwmError(ERR_INVALID_ARG, f"{where}: {name} is {n}")
+    return n
+
+
 def _kv8_group(where, q, H):
     """Query heads of q [B,Hq,D], a multiple of the cache's H heads."""
     shape = q.shape
@@ -778,9 +787,7 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
             return kv8_read(cache, start, T, kv_len, k_rot, v)
     w = "kv8_read"
     B, H, L, D, code = _kv8_sizes(w, cache)
-    T = int(T)
-    if T < 0:
-        raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
+    T = _kv8_count(w, "T", T, 0)
     shape = (B, T, H, D)
     dev = _kv8_ready(w, cache, (B, H, L, D), None,
                      (("start", start, (B,), torch.int32),
@@ -814,9 +821,9 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     w = "kv8_select"
     B, H, L, D, _ = _kv8_sizes(w, cache)
     Hq = _kv8_group(w, q, H)
-    K = int(n_select)
-    if K < 1:
-        raise LwmError(ERR_INVALID_ARG, f"{w}: n_select is {K}")
+    K = _kv8_count(w, "n_select", n_select, 1)
+    n_sink = _kv8_count(w, "n_sink", n_sink, 0)
+    n_recent = _kv8_count(w, "n_recent", n_recent, 0)
     lists = (B, H, K)
     dev = _kv8_ready(
         w, cache, (B, H, L, D), table,
@@ -834,14 +841,16 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
         q.data_ptr(), cache.k_bounds.data_ptr(), cache.k_scale.data_ptr(),
         kv_start.data_ptr(), kv_len.data_ptr(), q_pos.data_ptr(),
         table.data_ptr(), table.shape[0], B, L, Hq, H, D, DTYPE_BF16,
-        _layout_code(rope_layout), K, int(n_sink), int(n_recent),
+        _layout_code(rope_layout), K, n_sink, n_recent,
         blocks.data_ptr(), scores.data_ptr()))
     return blocks, scores
 
 
 def kv8_decode_workspace_size(B, L, Hq, H, n_blocks=None, D=HEAD_DIM) -> int:
-    return int(lib().lwm_kv8_decode_workspace_size(
-        B, L, Hq, H, D, -1 if n_blocks is None else n_blocks))
+    sizes = (B, L, Hq, H, D, -1 if n_blocks is None else n_blocks)
+    if not all(-(1 << 31) <= n < 1 << 31 for n in sizes):
+        return 0                            # as any size the library refuses
+    return int(lib().lwm_kv8_decode_workspace_size(*sizes))
 
 
 @functools.lru_cache(maxsize=1024)
