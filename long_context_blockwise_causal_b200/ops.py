@@ -731,6 +731,14 @@ def _kv8_ready(where, cache, sizes, table, tensors):
     return dev
 
 
+def _kv8_stream(where, cache, stream):
+    """The context of a call on a stream that the caller names."""
+    if stream.device != cache.k.device:
+        raise LwmError(ERR_INVALID_ARG, f"{where}: the cache is on "
+                       f"{cache.k.device}, the stream on {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def _kv8_call(name, call, dev, args):
     """call(*args, stream) with the tensors' device current, on that device's
     current stream."""
@@ -751,7 +759,7 @@ def kv8_write(cache, k, v, positions, start, table, n_new=None,
     start[b] + t (in place; see the header for the block scales). ``n_new``
     [B]: new tokens of a padded row. Returns the cache."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _kv8_stream("kv8_write", cache, stream):
             return kv8_write(cache, k, v, positions, start, table, n_new,
                              rope_layout)
     w = "kv8_write"
@@ -783,7 +791,7 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
     queries being given head i // (Hq // H):
     ``k_rot.repeat_interleave(Hq // H, 2)``."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _kv8_stream("kv8_read", cache, stream):
             return kv8_read(cache, start, T, kv_len, k_rot, v)
     w = "kv8_read"
     B, H, L, D, code = _kv8_sizes(w, cache)
@@ -814,7 +822,7 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     fp32) [B,H,n_select], ascending, (-1, -inf) behind a short list. The
     first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _kv8_stream("kv8_select", cache, stream):
             return kv8_select(q, cache, kv_start, kv_len, q_pos, table,
                               n_select, n_sink, n_recent, blocks, scores,
                               rope_layout)
@@ -869,7 +877,7 @@ def kv8_decode(q, cache, kv_start, kv_len, q_pos, table, blocks=None,
     [B,H,n] (a list of kv8_select, strictly ascending). Query head i reads
     cache head i // (Hq // H). Returns (out [B,Hq,D], lse [B,Hq])."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _kv8_stream("kv8_decode", cache, stream):
             return kv8_decode(q, cache, kv_start, kv_len, q_pos, table,
                               blocks, out, lse, workspace, rope_layout)
     w = "kv8_decode"
