@@ -89,7 +89,7 @@ struct Kv8DecodeArgs {
 };
 // CTAs of the decode kernel, and the floats of its partial results (K < 0:
 // no block list).
-int kv8_decode_grid(int B, int L, int H, int G, int K);
+int kv8_decode_grid(int B, int L, int H, int K);
 size_t kv8_part_floats(int B, int L, int H, int G, int K);
 cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st);
 

@@ -166,6 +166,7 @@ __host__ __device__ constexpr int part_stride(int G) {
 // the traffic is about 7 us: the walk to the first tile and its query (5 us
 // to the first scores), the last tile's product, and joining the parts (2).
 constexpr int kDecRing = 8;              // tile descriptions
+constexpr int kDecPerSm = 2;             // CTAs
 constexpr uint64_t kDecWaitNs = 4000000000ull;
 constexpr int kTile = kKv8Block * kHeadDim;   // bytes of K or V of one tile
 
@@ -187,7 +188,7 @@ struct Dec {
   static constexpr int kGroups = GP > 8 ? 2 : 1;        // of softmax warps
   static constexpr int kHeads = GP / kGroups;           // per group
   static constexpr int kThreads = 128 * kGroups + 64;
-  static constexpr int kPerSm = 2;                      // CTAs
+  static constexpr int kPerSm = kDecPerSm;
   static constexpr int kQTerms = kInt8 ? 3 : 5;
   static constexpr int kPTerms = kInt8 ? 3 : 4;
   static constexpr int kNq = (kQTerms * GP + 15) / 16 * 16;
@@ -240,7 +241,7 @@ struct Dec {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
-  static_assert(N == 1 || N == 2 || N == 4 || N == 8 || N == 16, "columns");
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "columns");
   if constexpr (N == 1) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
                  : "=r"(r[0]) : "r"(at));
@@ -250,21 +251,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
   } else if constexpr (N == 4) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
-  } else if constexpr (N == 8) {
+  } else {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, "
         "[%8];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
           "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(at));
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,"
-        "%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-          "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15])
         : "r"(at));
   }
 }
@@ -1177,18 +1169,16 @@ kv8_combine_cuts_kernel(const Kv8DecodeArgs a, int C) {
 
 }  // namespace
 
-int kv8_decode_grid(int B, int L, int H, int G, int K) {
+int kv8_decode_grid(int B, int L, int H, int K) {
   // every SM's CTAs at once, never more than there can be tiles
-  const int per_sm =
-      G > 8 ? Dec<false, 16>::kPerSm : Dec<false, 8>::kPerSm;
   const int64_t per = K >= 0 ? K : (L + kKv8Block - 1) / kKv8Block;
   const int64_t most = int64_t(B) * H * per;
   return int(
-      std::max<int64_t>(1, std::min<int64_t>(most, per_sm * sm_count())));
+      std::max<int64_t>(1, std::min<int64_t>(most, kDecPerSm * sm_count())));
 }
 
 size_t kv8_part_floats(int B, int L, int H, int G, int K) {
-  return size_t(kv8_decode_grid(B, L, H, G, K)) * 2 * part_stride(G);
+  return size_t(kv8_decode_grid(B, L, H, K)) * 2 * part_stride(G);
 }
 
 namespace {
@@ -1222,7 +1212,7 @@ cudaError_t launch_group(const Kv8DecodeArgs& a, int C, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv8_decode(const Kv8DecodeArgs& a, cudaStream_t st) {
-  const int C = kv8_decode_grid(a.B, a.L, a.H, a.G, a.listed ? a.K : -1);
+  const int C = kv8_decode_grid(a.B, a.L, a.H, a.listed ? a.K : -1);
   cudaError_t e =
       a.int8 ? launch_group<true>(a, C, st) : launch_group<false>(a, C, st);
   if (e != cudaSuccess) return e;

@@ -136,7 +136,7 @@ kv8_select_kernel(const __grid_constant__ Kv8SelectArgs a, int C) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = int(cluster_rank());
   const int64_t bh = blockIdx.x / C;
-  const int b = int(bh / a.H), h = int(bh - int64_t(b) * a.H);
+  const int b = int(bh / a.H);
   for (int i = t; i < kSelPasses * kSelBins; i += kSelThreads)
     hist[0][i] = 0;
   // a CTA that has arrived is running: its memory may be written

@@ -742,9 +742,10 @@ def _kv8_stream(where, cache, stream):
 def _kv8_call(name, call, dev, args):
     """call(*args, stream) with the tensors' device current, on that device's
     current stream."""
-    # (the current stream's handle, without building a Stream object)
+    # (the current stream's handle, without building a Stream object, which
+    # would be 1.2 us of a 12 us call)
     handle = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
+    if torch.cuda.current_device() == dev:
         st = call(*args, handle)
     else:
         with torch.cuda.device(dev):
