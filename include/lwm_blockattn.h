@@ -501,7 +501,15 @@ LWM_API int lwm_kv8_read(const void* k_cache, const void* v_cache,
  * to fp32; of the query heads that share a cache head the largest. The
  * first n_sink and the last n_recent visible blocks are always listed
  * (n_sink + n_recent <= n_select), then blocks whose score is NaN; ties go
- * to the lowest index. L <= 2^22. Async on stream. */
+ * to the lowest index. A query head that holds a NaN or an infinity scores 0
+ * everywhere. L <= 2^22. Async on stream.
+ * Scores order blocks and leave out what is the same for all of them: no key
+ * of the block has a score, in the units of lse, above
+ *   score * (Q / 127) / sqrt(D),
+ * Q as above (448/127 for an e4m3 cache, 1 for int8), but for the rounding
+ * of qi, which takes at most sum_d max(|lo_d|, |hi_d|) * k_scale * (a / 254)
+ * from score. Multiply by that factor before comparing scores with lse or
+ * with those of a cache of the other type. */
 LWM_API int lwm_kv8_select(const void* q, const int8_t* k_bounds,
                            const float* k_scale, const int32_t* kv_start,
                            const int32_t* kv_len, const int32_t* q_pos,

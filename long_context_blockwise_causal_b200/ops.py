@@ -821,7 +821,9 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     """The ``n_select`` blocks of 128 slots per (row, cache head) whose key
     bounds admit the largest scores for q [B,Hq,D]: (blocks int32, scores
     fp32) [B,H,n_select], ascending, (-1, -inf) behind a short list. The
-    first ``n_sink`` and last ``n_recent`` visible blocks are always in."""
+    first ``n_sink`` and last ``n_recent`` visible blocks are always in.
+    Scores are comparable within a call; times 448/127 (e4m3) or 1 (int8) and
+    1/sqrt(D) they are in the units of lse (see the header)."""
     if stream is not None:
         with _kv8_stream("kv8_select", cache, stream):
             return kv8_select(q, cache, kv_start, kv_len, q_pos, table,
