@@ -158,11 +158,13 @@ __host__ __device__ constexpr int part_stride(int G) {
 // on the next: S, P and, up to 8 heads, O are double buffered.
 //
 // Bound by HBM (256 bytes per slot and cache head) up to 8 query heads per
-// cache head: a 1M-slot cache of 32 heads in 1.16 ms (7.4 TB/s), 16 rows x
-// 32K x 8 heads in 161 us with 1 to 4 query heads each (6.7 TB/s) and 171 to
-// 173 with 8 (6.3); with 16 the softmax warps' instructions bound it (620 a
-// warp and tile; 233 us, int8 248). A kernel that decoded the codes on the
-// CUDA cores took 18.8 ms for the 1M-slot cache. What a call costs beside
+// cache head: a 1M-slot cache of 32 heads in 1.17 ms call after call (7.3
+// TB/s; 1.24 in turns over three caches), 16 rows x 32K x 8 heads in 158 to
+// 161 us with 1 to 4 query heads each (6.7 TB/s) and 172 to 174 with 8 (6.2);
+// with 16 the softmax warps' instructions bound it (665 a warp and tile; 246
+// to 260 us, int8 250 to 257; an e4m3 weight of three terms, one fewer than
+// now, 626 and 240). A kernel that decoded the codes on the CUDA cores took
+// 18.8 ms for the 1M-slot cache. What a call costs beside
 // the traffic is about 7 us: the walk to the first tile and its query (5 us
 // to the first scores), the last tile's product, and joining the parts (2).
 constexpr int kDecRing = 8;              // tile descriptions
@@ -213,7 +215,8 @@ struct Dec {
   // With three stages, a K tile is refilled together with its V tile: the
   // two then load side by side, 7.4 TB/s from a 1M-token cache, where
   // refilling it as soon as its scores are done gave 7.1. With fewer, the
-  // earlier refill wins (16 heads, 16 x 32K: 233 against 264 us).
+  // earlier refill wins (16 heads, 16 x 32K, weights of three terms: 233
+  // against 264 us).
   static constexpr int kRoom = 233472 / kPerSm - 2048 - kSmall;
   static constexpr int kTiles = kRoom / kTile < 6 ? kRoom / kTile : 6;
   static constexpr int kKStages = kTiles / 2, kVStages = kTiles - kKStages;

@@ -103,12 +103,14 @@ __device__ __forceinline__ int sum16(int (&v)[N]) {
 // the visible blocks into the shared memory of the first CTA, which finds
 // the K-th best key by three rounds of digit counting and writes the list;
 // counting over the shares of all CTAs cost more in exchanges (23 us for
-// three rounds over 8 CTAs) than one CTA takes for everything. Scoring is
-// bound by reading the bounds (256 bytes per block): 16 lanes share a block,
-// a warp keeps several pairs of blocks in flight, the first of them while
-// the query is made ready: 1M slots x 32 heads (67 MB) in 18 us, of which
-// scoring 16 and choosing 512 of 8192 blocks 2; 4 rows x 8 heads x 32K with
-// 4 query heads each in 6.7 us (latency). GP: G rounded up to a power of two.
+// three rounds over 8 CTAs) than one CTA takes for everything. Scoring reads
+// 256 bytes per block: 16 lanes share a block, a warp keeps several pairs of
+// blocks in flight, the first of them while the query is made ready. 1M slots
+// x 32 heads (67 MB) take 23.6 us in turns over eight caches, 18.2 where the
+// bounds are still in L2; 2 of them go to the digits of 512 of 8192 blocks
+// (a list that takes every block needs none). 4 rows x 8 heads x 32K with 4
+// query heads each are latency: 6.7 us, of which 3.3 for a call of a single
+// block, 2.2 for the digits. GP: G rounded up to a power of two.
 template <int GP, int Threads>
 struct Sel {
   // 512 threads, one CTA per SM, for few long rows; 256 threads, four CTAs
@@ -480,10 +482,14 @@ cudaError_t launch_rows(const Kv8SelectArgs& a, int C, cudaStream_t st) {
 }
 
 // Few (row, head) pairs: a cluster of large CTAs each, as long as there are
-// SMs for all of them at once and 128 blocks for each (32 heads of 1M slots:
-// 26 us over clusters of 4 where clusters of 8, in two rounds, took 37).
-// Many pairs, or short rows: one small CTA each, four to an SM (16 rows x 32
-// heads x 32K: 11.5 us; two large ones to an SM took 17.8).
+// SMs for all of them at once and more than 64 blocks for each. In turns over
+// caches that do not fit L2: 32 pairs of 1M slots 23.6 us over clusters of 4,
+// 30 over 2, 33.6 over 8 (two rounds); 8 pairs with 4 query heads each 21.5
+// over 8, 29 over 4; 32 pairs of 256 blocks 6.6 over 2, 7.1 in one small CTA
+// each; at 129 blocks that is even (6.1 and 5.6 for 8 pairs). More than 512
+// blocks of as many pairs as SMs: one large CTA each (128 pairs of 1024 blocks
+// 12.6, small ones 19.2). Many pairs, or short rows: one small CTA each, four
+// to an SM (512 pairs of 256 blocks 12.8 us, large ones 27).
 template <int GP>
 cudaError_t launch_group(const Kv8SelectArgs& a, cudaStream_t st) {
   const int nblk = (a.L + kKv8Block - 1) / kKv8Block;
