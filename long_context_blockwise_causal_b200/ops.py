@@ -677,13 +677,8 @@ def _kv8_sizes(where, cache):
     return B, H, L, D, code
 
 
-def _kv8_count(where, name, n, least):
-    """n as a whole number from `least` to the largest C int (ctypes would
-    pass on the low 32 bits of a larger one)."""
-    n = int(n)
-    if not least <= n < 1 << 31:
-        raise LwmError(ERR_INVALID_ARG, f"{where}: {name} is {n}")
-    return n
+# Counts beyond a C int are refused: ctypes would pass on their low 32 bits.
+_C_INT = 1 << 31
 
 
 def _kv8_group(where, q, H):
@@ -796,7 +791,9 @@ def kv8_read(cache, start, T, kv_len=None, k_rot=None, v=None, stream=None):
             return kv8_read(cache, start, T, kv_len, k_rot, v)
     w = "kv8_read"
     B, H, L, D, code = _kv8_sizes(w, cache)
-    T = _kv8_count(w, "T", T, 0)
+    T = int(T)
+    if not 0 <= T < _C_INT:
+        raise LwmError(ERR_INVALID_ARG, f"{w}: T is {T}")
     shape = (B, T, H, D)
     dev = _kv8_ready(w, cache, (B, H, L, D), None,
                      (("start", start, (B,), torch.int32),
@@ -832,9 +829,11 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
     w = "kv8_select"
     B, H, L, D, _ = _kv8_sizes(w, cache)
     Hq = _kv8_group(w, q, H)
-    K = _kv8_count(w, "n_select", n_select, 1)
-    n_sink = _kv8_count(w, "n_sink", n_sink, 0)
-    n_recent = _kv8_count(w, "n_recent", n_recent, 0)
+    K, n_sink, n_recent = int(n_select), int(n_sink), int(n_recent)
+    if not (1 <= K < _C_INT and 0 <= n_sink < _C_INT
+            and 0 <= n_recent < _C_INT):
+        raise LwmError(ERR_INVALID_ARG, f"{w}: {K} blocks, the first "
+                       f"{n_sink} and the last {n_recent} always")
     lists = (B, H, K)
     dev = _kv8_ready(
         w, cache, (B, H, L, D), table,
@@ -859,7 +858,7 @@ def kv8_select(q, cache, kv_start, kv_len, q_pos, table, n_select, n_sink=1,
 
 def kv8_decode_workspace_size(B, L, Hq, H, n_blocks=None, D=HEAD_DIM) -> int:
     sizes = (B, L, Hq, H, D, -1 if n_blocks is None else n_blocks)
-    if not all(-(1 << 31) <= n < 1 << 31 for n in sizes):
+    if not all(-_C_INT <= n < _C_INT for n in sizes):
         return 0                            # as any size the library refuses
     return int(lib().lwm_kv8_decode_workspace_size(*sizes))
 
